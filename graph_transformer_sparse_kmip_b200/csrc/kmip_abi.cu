@@ -28,6 +28,15 @@ int g_sm_count[kMaxDevices] = {};
 cudaMemPool_t g_pool[kMaxDevices] = {};
 uint64_t g_pool_keep[kMaxDevices] = {};
 
+// While a stream is being captured (by this thread, or by any thread in the
+// global mode), pool and symbol queries are refused and end the capture.
+// They touch no captured work here, so this thread is exempted around them.
+struct CaptureExempt {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  CaptureExempt() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~CaptureExempt() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 }  // namespace
 
 // Device address of g_status on the current device (resolved once per device).
@@ -36,6 +45,7 @@ int* status_ptr() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
   std::lock_guard<std::mutex> lock(g_mu);
   if (!g_status_ptr[dev]) {
+    CaptureExempt exempt;
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) return nullptr;
     g_status_ptr[dev] = static_cast<int*>(p);
@@ -65,11 +75,14 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // keeps, between calls, the most memory it has held (its release threshold
 // follows its largest reservation), so a loop of calls maps device memory
 // once instead of on every call, and it leaves the device's default pool,
-// which other code in the process may use, alone.
+// which other code in the process may use, alone.  On a capturing stream the
+// allocation becomes a memory node of the graph: each replay has its own
+// scratch, whatever else runs.
 cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
     return cudaErrorInvalidDevice;
+  CaptureExempt exempt;
   cudaMemPool_t pool = nullptr;
   {
     std::lock_guard<std::mutex> lock(g_mu);
