@@ -21,11 +21,14 @@ LIB_PATH = os.path.join(_PKG, "libkmip_debug.so" if os.environ.get("KMIP_DEBUG_B
 _NVTX = os.environ.get("KMIP_NVTX") == "1"
 
 KMIP_BF16, KMIP_F32 = 0, 1
+POS_TYPES = {torch.float32: 0, torch.int32: 1, torch.int64: 2}
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
 STATUS_NAMES = {0: "KMIP_OK", 1: "KMIP_ERR_INVALID_ARG", 2: "KMIP_ERR_UNSUPPORTED",
                 3: "KMIP_ERR_CUDA", 4: "KMIP_ERR_BAD_OFFSETS", 5: "KMIP_ERR_TIMEOUT",
                 6: "KMIP_ERR_BAD_INDEX", 7: "KMIP_ERR_SCRATCH_LIMIT"}
 EXPORTED = ("kmip_attn_fwd", "kmip_attn_fwd_noalloc", "kmip_attn_fwd_diag", "kmip_attn_bwd",
             "kmip_attn_bwd_deterministic", "kmip_attn_gather", "kmip_get_status",
+            "kmip_rotary", "kmip_group_norm_fwd", "kmip_group_norm_bwd",
             "kmip_scratch_usage", "kmip_scratch_trim", "kmip_error_string",
             "kmip_fwd_path", "kmip_version")
 
@@ -61,6 +64,14 @@ def load() -> ctypes.CDLL:
     lib.kmip_attn_bwd_deterministic.restype = I32
     lib.kmip_attn_gather.argtypes = [P, P, P, P, I64, I32, I32, I32, F32, P, P, P, I32]
     lib.kmip_attn_gather.restype = I32
+    lib.kmip_rotary.argtypes = [P, I64, I64, P, I32, I32, P, P, I32, I32, I32, I64, I32, I32, P,
+                                I64, I64, P, I32]
+    lib.kmip_rotary.restype = I32
+    lib.kmip_group_norm_fwd.argtypes = [P, P, P, P, I64, I32, I32, F32, I32, P, P, P, P, I32, I32]
+    lib.kmip_group_norm_fwd.restype = I32
+    lib.kmip_group_norm_bwd.argtypes = [P, P, P, P, P, P, P, I64, I32, I32, I32, P, P, P, P, I32,
+                                        I32]
+    lib.kmip_group_norm_bwd.restype = I32
     lib.kmip_get_status.argtypes = [P]
     lib.kmip_get_status.restype = I32
     lib.kmip_scratch_usage.argtypes = [P, P, I32]
@@ -295,6 +306,129 @@ def attn_bwd(dOut, Q, K, V, idx, lse, scale: float, stream=None, deterministic=F
     if rc:
         raise KmipError(rc, fn.__name__)
     return dQ, dK, dV
+
+
+# --- the operators around the attention: positions, norm, feed-forward ---
+
+def _same_device(x, *ts):
+    """Every tensor on x's CUDA device, contiguous (x itself may be strided)."""
+    if not x.is_cuda:
+        raise ValueError("libkmip takes CUDA tensors")
+    for t in ts:
+        if t is not None and (t.device != x.device or not t.is_contiguous()):
+            raise ValueError(f"expected a contiguous tensor on {x.device}")
+
+
+def _expect(t, name, shape, dtype):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+
+
+def _act_code(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r} (one of {', '.join(ACTS)})")
+    return ACTS[act]
+
+
+def _offsets(graph_offsets):
+    """Checks graph_offsets (int32 [G+1] or None); returns G."""
+    if graph_offsets is None:
+        return 1
+    if graph_offsets.dtype != torch.int32 or graph_offsets.dim() != 1 or graph_offsets.numel() < 2:
+        raise ValueError("graph_offsets: expected int32 [G + 1] with G >= 1")
+    return graph_offsets.numel() - 1
+
+
+def _launch(x, name, *args, stream=None):
+    """Calls entry point `name` with x's device current; `stream` goes where
+    the argument list says _STREAM.  Raises on a status."""
+    with torch.cuda.device(x.device):
+        s = _stream(stream)
+        rc = _call(name, *(s if a is _STREAM else a for a in args))
+    if rc:
+        raise KmipError(rc, name)
+
+
+_STREAM = object()
+
+
+def rotary(x, pos, freq, axis, inverse: bool = False, interleaved: bool = False, out=None,
+           stream=None):
+    """Rotary positions with several axes (kmip_rotary): pair p of every head
+    of node n turns by pos[n, axis[p]] * freq[p].
+
+    x: [N, H, d] bf16 or fp32, rows and heads at any stride, elements of a
+    head adjacent; pos: [N, A] fp32, int32 or int64; freq: fp64 [P]; axis:
+    int32 [P].  out: a new contiguous tensor, or a tensor like x (x itself:
+    in place).  inverse=True is the gradient with respect to x."""
+    if x.dim() != 3 or (x.shape[2] > 1 and x.numel() and x.stride(2) != 1):
+        raise ValueError("x: expected [N, H, d] with adjacent elements in a head")
+    N, H, d = x.shape
+    if pos.dtype not in POS_TYPES:
+        raise TypeError(f"unsupported position dtype {pos.dtype} (fp32, int32 or int64)")
+    if pos.dim() != 2 or pos.shape[0] != N:
+        raise ValueError(f"pos: expected [{N}, axes], got {tuple(pos.shape)}")
+    P = freq.numel()
+    _expect(freq, "freq", (P,), torch.float64)
+    _expect(axis, "axis", (P,), torch.int32)
+    _same_device(x, pos, freq, axis)
+    if out is None:
+        out = torch.empty((N, H, d), dtype=x.dtype, device=x.device)
+    elif (out.shape != x.shape or out.dtype != x.dtype or out.device != x.device
+          or (d > 1 and out.numel() and out.stride(2) != 1)):
+        raise ValueError("out: expected a tensor like x")
+    _launch(x, "kmip_rotary", _ptr(x), x.stride(0), x.stride(1), _ptr(pos), POS_TYPES[pos.dtype],
+            pos.shape[1], _ptr(freq), _ptr(axis), P, int(bool(interleaved)), int(bool(inverse)),
+            N, H, d, _ptr(out), out.stride(0), out.stride(1), _STREAM, dtype_code(x.dtype),
+            stream=stream)
+    return out
+
+
+def group_norm_fwd(x, weight, bias, groups: int, eps: float = 1e-5, act: str = "none",
+                   graph_offsets=None, stream=None):
+    """Group norm per graph with an activation (kmip_group_norm_fwd).
+
+    x: [N, C] bf16 or fp32, contiguous; weight, bias: [C] like x, or both
+    None; graph_offsets: int32 [G+1] or None (one graph).  Returns (y,
+    mean, rstd), the last two fp32 [G, groups]."""
+    if x.dim() != 2:
+        raise ValueError("x: expected [N, C]")
+    N, C = x.shape
+    G = _offsets(graph_offsets)
+    _same_device(x, x, weight, bias, graph_offsets)
+    _expect(weight, "weight", (C,), x.dtype)
+    _expect(bias, "bias", (C,), x.dtype)
+    y = torch.empty_like(x)
+    mean = torch.empty((G, groups), dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    _launch(x, "kmip_group_norm_fwd", _ptr(x), _ptr(weight), _ptr(bias), _ptr(graph_offsets), N,
+            C, groups, float(eps), _act_code(act), _ptr(y), _ptr(mean), _ptr(rstd), _STREAM, G,
+            dtype_code(x.dtype), stream=stream)
+    return y, mean, rstd
+
+
+def group_norm_bwd(dy, x, weight, bias, mean, rstd, groups: int, act: str = "none",
+                   graph_offsets=None, stream=None):
+    """Backward of group_norm_fwd: (dx, dweight, dbias) in x's type; the last
+    two are None when there is no weight."""
+    if x.dim() != 2:
+        raise ValueError("x: expected [N, C]")
+    N, C = x.shape
+    G = _offsets(graph_offsets)
+    _same_device(x, x, dy, weight, bias, graph_offsets, mean, rstd)
+    _expect(dy, "dy", (N, C), x.dtype)
+    _expect(weight, "weight", (C,), x.dtype)
+    _expect(bias, "bias", (C,), x.dtype)
+    _expect(mean, "mean", (G, groups), torch.float32)
+    _expect(rstd, "rstd", (G, groups), torch.float32)
+    dx = torch.empty_like(x)
+    dw = db = None
+    if weight is not None:
+        dw, db = torch.empty_like(weight), torch.empty_like(weight)
+    _launch(x, "kmip_group_norm_bwd", _ptr(dy), _ptr(x), _ptr(weight), _ptr(bias),
+            _ptr(graph_offsets), _ptr(mean), _ptr(rstd), N, C, groups, _act_code(act), _ptr(dx),
+            _ptr(dw), _ptr(db), _STREAM, G, dtype_code(x.dtype), stream=stream)
+    return dx, dw, db
 
 
 def check_status(stream=None):

@@ -48,6 +48,8 @@
  *     fp32; dQ, dK, dV are [N, H, d] fp32.
  *   - Calls are asynchronous on `stream` (NULL = legacy default stream).
  *     A non-OK status returned by a call means nothing was enqueued.
+ *     Calls may be captured into CUDA graphs (kmip_get_status may not: it
+ *     synchronises); a captured call's scratch belongs to the graph.
  *   - Errors found on the device (malformed graph_offsets, an index out of
  *     range, a pipeline wait that ran out) are recorded in a per-device
  *     status word and reported by kmip_get_status(); outputs of the affected
@@ -252,6 +254,97 @@ kmip_status_t kmip_scratch_usage(uint64_t* reserved, uint64_t* used_high, int re
  * Returns KMIP_OK (also when the pool does not exist yet) or KMIP_ERR_CUDA.
  */
 kmip_status_t kmip_scratch_trim(void);
+
+/* ------------------------------------------------------------------------
+ * The operators around the attention in a GraphGPS layer (k-Maximum Inner
+ * Product Attention for Graph Transformers ..., Figure 1: a layer is a local
+ * branch and the attention branch, normalised, added and passed through a
+ * feed-forward part).  The conventions above hold (device pointers on the
+ * current device, asynchronous on `stream`, scratch from the library's pool);
+ * what differs is said at each call.
+ * ---------------------------------------------------------------------- */
+
+/* Element type of a position array. */
+typedef enum { KMIP_POS_F32 = 0, KMIP_POS_I32 = 1, KMIP_POS_I64 = 2 } kmip_pos_t;
+
+/* Activations: none; silu z sigmoid(z); gelu z Phi(z) (the exact one, by the
+ * error function); relu max(z, 0). */
+typedef enum {
+  KMIP_ACT_NONE = 0,
+  KMIP_ACT_SILU = 1,
+  KMIP_ACT_GELU = 2,
+  KMIP_ACT_RELU = 3
+} kmip_act_t;
+
+/*
+ * Rotary positions with several axes.  Pair p (0 <= p < pairs) of every head
+ * of node n turns by the angle pos[n, axis[p]] * freq[p]:
+ *   (u, v) -> (u cos - v sin, u sin + v cos)
+ * where (u, v) are elements (p, p + pairs) of the head, or (2p, 2p + 1) when
+ * `interleaved`.  Elements behind 2 * pairs are copied.  `inverse` turns by
+ * the negative angle: that is the backward pass with respect to x.
+ *   x          N rows of H heads of d elements; element (n, h, e) is at
+ *              x[n * x_row + h * x_head + e] (strides in elements, so q and k
+ *              can be turned where a fused projection wrote them).
+ *   pos        [N, axes] of pos_type.
+ *   freq       double [pairs], radians per unit; axis int32 [pairs], each in
+ *              [0, axes).  An entry outside records KMIP_ERR_BAD_INDEX and its
+ *              pair is left unturned.
+ *   out        as x with its own strides; out == x (with the same strides)
+ *              turns in place, otherwise the two may not overlap.
+ * Angles are formed and reduced in fp64, so positions far from zero keep
+ * their angle; the turn itself is fp32, rounded once.
+ * Supported: d even, 2..512; H <= 4096; axes <= 64; 0 <= 2 pairs <= d.  x and
+ * out need only their element's alignment (interleaved: a pair's, and even
+ * strides); 16-byte aligned rows and heads are the fast case.
+ */
+kmip_status_t kmip_rotary(const void* x, int64_t x_row, int64_t x_head, const void* pos,
+                          kmip_pos_t pos_type, int axes, const double* freq,
+                          const int32_t* axis, int pairs, int interleaved, int inverse,
+                          int64_t N, int H, int d, void* out, int64_t out_row,
+                          int64_t out_head, kmip_stream_t stream, kmip_dtype_t dtype);
+
+/*
+ * Group norm per graph with an activation, channels last.  With C channels in
+ * `groups` groups of C / groups consecutive ones, for graph g and group j
+ *   mean, var  over the nodes of g and the channels of j (biased variance)
+ *   rstd     = 1 / sqrt(var + eps)
+ *   y        = act((x - mean) * rstd * weight + bias)
+ *   x, y       [N, C] of `dtype` row-major; y may be x.
+ *   weight, bias  [C] of `dtype`, or both NULL (1 and 0).
+ *   graph_offsets as in kmip_attn_fwd (NULL: one graph).  Each graph's range
+ *              is checked on the device: a malformed one records
+ *              KMIP_ERR_BAD_OFFSETS; y, mean and rstd are then unspecified.
+ *   mean, rstd fp32 [num_graphs, groups], overwritten (an empty graph: 0 and
+ *              1 / sqrt(eps)); the backward takes them.
+ * Statistics are held in fp32 (per thread, by batches with their own mean)
+ * and joined in fp64; results do not change from run to run.
+ * Supported: 1 <= groups <= C <= 65536, groups divides C; eps > 0.  x, y and
+ * the parameters need only their element's alignment; 16-byte aligned rows
+ * with C / groups a multiple of 8 (bf16) or 4 (fp32) are the fast case.
+ */
+kmip_status_t kmip_group_norm_fwd(const void* x, const void* weight, const void* bias,
+                                  const int32_t* graph_offsets, int64_t N, int C, int groups,
+                                  float eps, kmip_act_t act, void* y, float* mean, float* rstd,
+                                  kmip_stream_t stream, int num_graphs, kmip_dtype_t dtype);
+
+/*
+ * Backward of kmip_group_norm_fwd; mean and rstd are its outputs.  With z the
+ * argument of the activation, xhat = (x - mean) rstd and dz = dy act'(z):
+ *   dbias   = sum over all nodes of dz         (of `dtype`, [C])
+ *   dweight = sum over all nodes of dz xhat    (of `dtype`, [C])
+ *   dx      = rstd (dz weight - m1 - xhat m2)  (of `dtype`, [N, C])
+ * m1, m2 = means of dz weight and dz weight xhat over the graph and group.
+ * dweight and dbias are written when weight is given (then they may not be
+ * NULL).  dx may be dy, and may not be x.  Sums are joined in a fixed order:
+ * results do not change from run to run.
+ */
+kmip_status_t kmip_group_norm_bwd(const void* dy, const void* x, const void* weight,
+                                  const void* bias, const int32_t* graph_offsets,
+                                  const float* mean, const float* rstd, int64_t N, int C,
+                                  int groups, kmip_act_t act, void* dx, void* dweight,
+                                  void* dbias, kmip_stream_t stream, int num_graphs,
+                                  kmip_dtype_t dtype);
 
 /* Static, human-readable name of a status code (never NULL). */
 const char* kmip_error_string(kmip_status_t status);

@@ -1,0 +1,93 @@
+"""Refusals of the operators around the attention, checked on the host: the
+entry points return a status before they touch a device, and the binding
+raises on tensors it cannot pass."""
+import ctypes
+
+import pytest
+import torch
+
+from graph_transformer_sparse_kmip_b200 import binding
+
+INVALID, UNSUP = 1, 2
+A = 1 << 20  # an aligned address that is never read
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from graph_transformer_sparse_kmip_b200 import build
+    build.build()
+    return binding.load()
+
+
+def _rotary(lib, x=A, x_row=64, x_head=32, pos=A, pos_type=0, axes=2, freq=A, axis=A, pairs=16,
+            inter=0, N=4, H=2, d=32, out=2 * A, out_row=64, out_head=32, dtype=0):
+    return lib.kmip_rotary(x, x_row, x_head, pos, pos_type, axes, freq, axis, pairs, inter, 0, N,
+                           H, d, out, out_row, out_head, None, dtype)
+
+
+def test_rotary_refusals(lib):
+    for kw in (dict(N=-1), dict(N=1 << 31), dict(H=0), dict(d=0), dict(axes=0), dict(pairs=-1),
+               dict(pairs=17), dict(dtype=2), dict(pos_type=3), dict(x=None), dict(out=None),
+               dict(pos=None), dict(freq=None), dict(axis=None), dict(x=A + 1), dict(out=A + 1),
+               dict(inter=1, x=A + 2), dict(dtype=1, x=A + 2), dict(x_row=-64), dict(x_head=-1),
+               # in place needs the same strides
+               dict(out=A, out_head=64, out_row=128),
+               # heads or rows of the output that share elements
+               dict(out_head=31), dict(out_row=63), dict(out_row=0), dict(H=1, out_row=16),
+               dict(out_row=32, out_head=100)):
+        assert _rotary(lib, **kw) == INVALID, kw
+    for kw in (dict(d=33), dict(d=514), dict(H=4097, out_row=4097 * 32), dict(axes=65),
+               dict(inter=1, x_row=65), dict(inter=1, x_head=33)):
+        assert _rotary(lib, **kw) == UNSUP, kw
+    assert _rotary(lib, N=0, x=None, out=None, pos=None) == 0
+
+
+def _norm_fwd(lib, x=A, w=A, b=A, off=None, N=8, C=32, groups=4, eps=1e-5, act=1, y=A, mean=A,
+              rstd=A, G=1, dtype=0):
+    return lib.kmip_group_norm_fwd(x, w, b, off, N, C, groups, eps, act, y, mean, rstd, None, G,
+                                   dtype)
+
+
+def _norm_bwd(lib, dy=A, x=A, w=A, b=A, off=None, mean=A, rstd=A, N=8, C=32, groups=4, act=1,
+              dx=2 * A, dw=A, db=A, G=1, dtype=0):
+    return lib.kmip_group_norm_bwd(dy, x, w, b, off, mean, rstd, N, C, groups, act, dx, dw, db,
+                                   None, G, dtype)
+
+
+def test_group_norm_refusals(lib):
+    nan, inf = float("nan"), float("inf")
+    both = (dict(N=-1), dict(N=1 << 31), dict(C=0), dict(groups=0), dict(groups=5),
+            dict(groups=64), dict(act=4), dict(act=-1), dict(dtype=3), dict(off=A, G=0),
+            dict(x=None), dict(w=None), dict(b=None), dict(mean=None), dict(rstd=None),
+            dict(x=A + 1), dict(dtype=1, w=A + 2))
+    for kw in both + (dict(eps=0.0), dict(eps=-1.0), dict(eps=nan), dict(eps=inf), dict(y=None)):
+        assert _norm_fwd(lib, **kw) == INVALID, kw
+    for kw in both + (dict(dy=None), dict(dx=None), dict(dw=None), dict(db=None), dict(dx=A)):
+        assert _norm_bwd(lib, **kw) == INVALID, kw
+    for kw in (dict(C=65537, groups=1), dict(N=(1 << 31) - 1, C=1024)):
+        assert _norm_fwd(lib, **kw) == UNSUP and _norm_bwd(lib, **kw) == UNSUP, kw
+
+
+def test_binding_refuses_what_it_cannot_pass():
+    x = torch.zeros(4, 2, 32)
+    pos, freq = torch.zeros(4, 2), torch.zeros(16, dtype=torch.float64)
+    axis = torch.zeros(16, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.rotary(x, pos, freq, axis)
+    with pytest.raises(ValueError, match="adjacent"):
+        binding.rotary(x.transpose(1, 2), pos, freq, axis)
+    with pytest.raises(TypeError, match="position"):
+        binding.rotary(x, pos.double(), freq, axis)
+    with pytest.raises(ValueError, match="pos"):
+        binding.rotary(x, pos[:3], freq, axis)
+    with pytest.raises(ValueError, match="freq"):
+        binding.rotary(x, pos, freq.float(), axis)
+    with pytest.raises(ValueError, match="axis"):
+        binding.rotary(x, pos, freq, axis[:8])
+    y, w = torch.zeros(6, 32), torch.ones(32)
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.group_norm_fwd(y, w, w, 4)
+    with pytest.raises(ValueError, match="N, C"):
+        binding.group_norm_fwd(y[0], w, w, 4)
+    with pytest.raises(ValueError, match="graph_offsets"):
+        binding.group_norm_fwd(y, w, w, 4, graph_offsets=torch.tensor([0, 6]))
