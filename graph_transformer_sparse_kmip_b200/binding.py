@@ -29,6 +29,7 @@ STATUS_NAMES = {0: "KMIP_OK", 1: "KMIP_ERR_INVALID_ARG", 2: "KMIP_ERR_UNSUPPORTE
 EXPORTED = ("kmip_attn_fwd", "kmip_attn_fwd_noalloc", "kmip_attn_fwd_diag", "kmip_attn_bwd",
             "kmip_attn_bwd_deterministic", "kmip_attn_gather", "kmip_get_status",
             "kmip_rotary", "kmip_group_norm_fwd", "kmip_group_norm_bwd",
+            "kmip_ffn_fwd", "kmip_ffn_bwd",
             "kmip_scratch_usage", "kmip_scratch_trim", "kmip_error_string",
             "kmip_fwd_path", "kmip_version")
 
@@ -72,6 +73,10 @@ def load() -> ctypes.CDLL:
     lib.kmip_group_norm_bwd.argtypes = [P, P, P, P, P, P, P, I64, I32, I32, I32, P, P, P, P, I32,
                                         I32]
     lib.kmip_group_norm_bwd.restype = I32
+    lib.kmip_ffn_fwd.argtypes = [P, P, P, P, I64, I32, I32, I32, P, P, I32]
+    lib.kmip_ffn_fwd.restype = I32
+    lib.kmip_ffn_bwd.argtypes = [P, P, P, P, P, I64, I32, I32, I32, P, P, P, P, P, I32]
+    lib.kmip_ffn_bwd.restype = I32
     lib.kmip_get_status.argtypes = [P]
     lib.kmip_get_status.restype = I32
     lib.kmip_scratch_usage.argtypes = [P, P, I32]
@@ -429,6 +434,40 @@ def group_norm_bwd(dy, x, weight, bias, mean, rstd, groups: int, act: str = "non
             _ptr(graph_offsets), _ptr(mean), _ptr(rstd), N, C, groups, _act_code(act), _ptr(dx),
             _ptr(dw), _ptr(db), _STREAM, G, dtype_code(x.dtype), stream=stream)
     return dx, dw, db
+
+
+def _ffn_args(x, wg, wu, wd):
+    if x.dim() != 2 or wg.dim() != 2:
+        raise ValueError("x: expected [N, C]; wg, wu: [F, C]; wd: [C, F]")
+    (N, C), F = x.shape, wg.shape[0]
+    _same_device(x, x, wg, wu, wd)
+    _expect(wg, "wg", (F, C), x.dtype)
+    _expect(wu, "wu", (F, C), x.dtype)
+    _expect(wd, "wd", (C, F), x.dtype)
+    return N, C, F
+
+
+def ffn_fwd(x, wg, wu, wd, act: str = "silu", stream=None):
+    """Gated feed-forward block y = (act(x wg^T) * (x wu^T)) wd^T
+    (kmip_ffn_fwd).  x: [N, C] bf16 or fp32; wg, wu: [F, C]; wd: [C, F]."""
+    N, C, F = _ffn_args(x, wg, wu, wd)
+    y = torch.empty_like(x)
+    _launch(x, "kmip_ffn_fwd", _ptr(x), _ptr(wg), _ptr(wu), _ptr(wd), N, C, F, _act_code(act),
+            _ptr(y), _STREAM, dtype_code(x.dtype), stream=stream)
+    return y
+
+
+def ffn_bwd(dy, x, wg, wu, wd, act: str = "silu", stream=None):
+    """Backward of ffn_fwd: (dx, dwg, dwu, dwd) in x's type."""
+    N, C, F = _ffn_args(x, wg, wu, wd)
+    _same_device(x, dy)
+    _expect(dy, "dy", (N, C), x.dtype)
+    dx = torch.empty_like(x)
+    dwg, dwu, dwd = torch.empty_like(wg), torch.empty_like(wu), torch.empty_like(wd)
+    _launch(x, "kmip_ffn_bwd", _ptr(dy), _ptr(x), _ptr(wg), _ptr(wu), _ptr(wd), N, C, F,
+            _act_code(act), _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(dwd), _STREAM,
+            dtype_code(x.dtype), stream=stream)
+    return dx, dwg, dwu, dwd
 
 
 def check_status(stream=None):

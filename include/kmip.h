@@ -346,6 +346,35 @@ kmip_status_t kmip_group_norm_bwd(const void* dy, const void* x, const void* wei
                                   void* dbias, kmip_stream_t stream, int num_graphs,
                                   kmip_dtype_t dtype);
 
+/*
+ * Gated feed-forward block:
+ *   y = (act(x Wg^T) * (x Wu^T)) Wd^T
+ *   x, y       [N, C] of `dtype` row-major;  Wg, Wu [F, C];  Wd [C, F].
+ * bf16 runs on the tcgen05 tensor cores with fp32 accumulation (the product
+ * h of the two projections is rounded to bf16 between the GEMMs); fp32 runs
+ * on fp32 fused multiply-adds.  Takes N F elements of scratch (fp32: 2 N F).
+ * Supported: C and F multiples of 8, 8 .. 65536; all pointers 16-byte
+ * aligned; y may not overlap an input.
+ */
+kmip_status_t kmip_ffn_fwd(const void* x, const void* Wg, const void* Wu, const void* Wd,
+                           int64_t N, int C, int F, kmip_act_t act, void* y,
+                           kmip_stream_t stream, kmip_dtype_t dtype);
+
+/*
+ * Backward of kmip_ffn_fwd: from dy and the forward's inputs
+ *   dx [N, C], dWg, dWu [F, C], dWd [C, F], all of `dtype`, overwritten.
+ * Nothing is kept from the forward: both projections are computed again, in
+ * fp32 accumulators that meet dy Wd there, so the one rounding to bf16 before
+ * the gradients is that of the projections' gradients and h.  Takes 3 N F
+ * elements of scratch and at most 78 MB of partial sums, which are joined in
+ * a fixed order: results do not change from run to run.  N = 0 gives zero
+ * weight gradients.  Outputs may not overlap inputs or one another.
+ */
+kmip_status_t kmip_ffn_bwd(const void* dy, const void* x, const void* Wg, const void* Wu,
+                           const void* Wd, int64_t N, int C, int F, kmip_act_t act, void* dx,
+                           void* dWg, void* dWu, void* dWd, kmip_stream_t stream,
+                           kmip_dtype_t dtype);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* kmip_error_string(kmip_status_t status);
 

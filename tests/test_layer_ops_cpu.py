@@ -68,6 +68,30 @@ def test_group_norm_refusals(lib):
         assert _norm_fwd(lib, **kw) == UNSUP and _norm_bwd(lib, **kw) == UNSUP, kw
 
 
+def _ffn_fwd(lib, x=A, wg=A, wu=A, wd=A, N=8, C=32, F=64, act=1, y=2 * A, dtype=0):
+    return lib.kmip_ffn_fwd(x, wg, wu, wd, N, C, F, act, y, None, dtype)
+
+
+def _ffn_bwd(lib, dy=A, x=A, wg=A, wu=A, wd=A, N=8, C=32, F=64, act=1, dx=2 * A, dwg=3 * A,
+             dwu=4 * A, dwd=5 * A, dtype=0):
+    return lib.kmip_ffn_bwd(dy, x, wg, wu, wd, N, C, F, act, dx, dwg, dwu, dwd, None, dtype)
+
+
+def test_ffn_refusals(lib):
+    both = (dict(N=-1), dict(N=1 << 31), dict(C=0), dict(F=0), dict(act=4), dict(act=-1),
+            dict(dtype=2), dict(x=None), dict(wg=None), dict(wu=None), dict(wd=None),
+            dict(x=A + 8), dict(wg=A + 2), dict(wd=A + 4))
+    for kw in both + (dict(y=None), dict(y=A + 8)):
+        assert _ffn_fwd(lib, **kw) == INVALID, kw
+    for kw in both + (dict(dy=None), dict(dx=None), dict(dwg=None), dict(dwu=None),
+                      dict(dwd=None), dict(dx=A + 8), dict(dwd=A + 8)):
+        assert _ffn_bwd(lib, **kw) == INVALID, kw
+    for kw in (dict(C=36), dict(F=60), dict(C=65544), dict(F=65544),
+               dict(N=(1 << 31) - 1, F=65536)):
+        assert _ffn_fwd(lib, **kw) == UNSUP and _ffn_bwd(lib, **kw) == UNSUP, kw
+    assert _ffn_fwd(lib, N=0, x=None, y=None) == 0
+
+
 def test_binding_refuses_what_it_cannot_pass():
     x = torch.zeros(4, 2, 32)
     pos, freq = torch.zeros(4, 2), torch.zeros(16, dtype=torch.float64)
@@ -91,3 +115,8 @@ def test_binding_refuses_what_it_cannot_pass():
         binding.group_norm_fwd(y[0], w, w, 4)
     with pytest.raises(ValueError, match="graph_offsets"):
         binding.group_norm_fwd(y, w, w, 4, graph_offsets=torch.tensor([0, 6]))
+    g, d = torch.zeros(64, 32), torch.zeros(32, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.ffn_fwd(y, g, g, d)
+    with pytest.raises(ValueError, match="expected"):
+        binding.ffn_fwd(y, g[0], g, d)
