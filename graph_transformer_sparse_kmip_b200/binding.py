@@ -315,17 +315,23 @@ def attn_bwd(dOut, Q, K, V, idx, lse, scale: float, stream=None, deterministic=F
 
 # --- the operators around the attention: positions, norm, feed-forward ---
 
+# A small call is bound by what happens before its launch: these helpers stay
+# with integers (device indices, addresses, raw stream handles) and make no
+# torch.device, torch.cuda.Stream or ctypes objects on the way.
+
 def _same_device(x, *ts):
-    """Every tensor on x's CUDA device, contiguous (x itself may be strided)."""
+    """Every tensor on x's CUDA device and contiguous (x itself may be
+    strided)."""
     if not x.is_cuda:
         raise ValueError("libkmip takes CUDA tensors")
+    dev = x.get_device()
     for t in ts:
-        if t is not None and (t.device != x.device or not t.is_contiguous()):
+        if t is not None and (not t.is_cuda or t.get_device() != dev or not t.is_contiguous()):
             raise ValueError(f"expected a contiguous tensor on {x.device}")
 
 
 def _expect(t, name, shape, dtype):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
 
 
@@ -344,17 +350,30 @@ def _offsets(graph_offsets):
     return graph_offsets.numel() - 1
 
 
-def _launch(x, name, *args, stream=None):
-    """Calls entry point `name` with x's device current; `stream` goes where
-    the argument list says _STREAM.  Raises on a status."""
-    with torch.cuda.device(x.device):
-        s = _stream(stream)
-        rc = _call(name, *(s if a is _STREAM else a for a in args))
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch(x, name, stream, args, tail):
+    """Calls entry point `name` with args, the stream and tail, with x's
+    device current: on `stream`, or on that device's current stream.  Raises
+    on a status."""
+    dev = x.get_device()
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(x, name, stream, args, tail)
+    if stream is not None:
+        s = stream.cuda_stream
+    elif _raw_stream is not None:
+        s = _raw_stream(dev)
+    else:
+        s = torch.cuda.current_stream().cuda_stream
+    rc = _call(name, *args, s, *tail)
     if rc:
         raise KmipError(rc, name)
-
-
-_STREAM = object()
 
 
 def rotary(x, pos, freq, axis, inverse: bool = False, interleaved: bool = False, out=None,
@@ -366,26 +385,29 @@ def rotary(x, pos, freq, axis, inverse: bool = False, interleaved: bool = False,
     head adjacent; pos: [N, A] fp32, int32 or int64; freq: fp64 [P]; axis:
     int32 [P].  out: a new contiguous tensor, or a tensor like x (x itself:
     in place).  inverse=True is the gradient with respect to x."""
-    if x.dim() != 3 or (x.shape[2] > 1 and x.numel() and x.stride(2) != 1):
-        raise ValueError("x: expected [N, H, d] with adjacent elements in a head")
-    N, H, d = x.shape
-    if pos.dtype not in POS_TYPES:
+    if x.dim() != 3:
+        raise ValueError("x: expected [N, H, d]")
+    (N, H, d), xs, P = x.shape, x.stride(), freq.numel()
+    if xs[2] != 1 and d > 1 and N * H:
+        raise ValueError("x: expected adjacent elements in a head")
+    pos_type = POS_TYPES.get(pos.dtype)
+    if pos_type is None:
         raise TypeError(f"unsupported position dtype {pos.dtype} (fp32, int32 or int64)")
     if pos.dim() != 2 or pos.shape[0] != N:
         raise ValueError(f"pos: expected [{N}, axes], got {tuple(pos.shape)}")
-    P = freq.numel()
     _expect(freq, "freq", (P,), torch.float64)
     _expect(axis, "axis", (P,), torch.int32)
     _same_device(x, pos, freq, axis)
     if out is None:
-        out = torch.empty((N, H, d), dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif (out.shape != x.shape or out.dtype != x.dtype or out.device != x.device
-          or (d > 1 and out.numel() and out.stride(2) != 1)):
+          or (out.stride(2) != 1 and d > 1 and N * H)):
         raise ValueError("out: expected a tensor like x")
-    _launch(x, "kmip_rotary", _ptr(x), x.stride(0), x.stride(1), _ptr(pos), POS_TYPES[pos.dtype],
-            pos.shape[1], _ptr(freq), _ptr(axis), P, int(bool(interleaved)), int(bool(inverse)),
-            N, H, d, _ptr(out), out.stride(0), out.stride(1), _STREAM, dtype_code(x.dtype),
-            stream=stream)
+    os = out.stride()
+    _launch(x, "kmip_rotary", stream,
+            (x.data_ptr(), xs[0], xs[1], pos.data_ptr(), pos_type, pos.shape[1], freq.data_ptr(),
+             axis.data_ptr(), P, bool(interleaved), bool(inverse), N, H, d, out.data_ptr(), os[0],
+             os[1]), (dtype_code(x.dtype),))
     return out
 
 
@@ -406,9 +428,10 @@ def group_norm_fwd(x, weight, bias, groups: int, eps: float = 1e-5, act: str = "
     y = torch.empty_like(x)
     mean = torch.empty((G, groups), dtype=torch.float32, device=x.device)
     rstd = torch.empty_like(mean)
-    _launch(x, "kmip_group_norm_fwd", _ptr(x), _ptr(weight), _ptr(bias), _ptr(graph_offsets), N,
-            C, groups, float(eps), _act_code(act), _ptr(y), _ptr(mean), _ptr(rstd), _STREAM, G,
-            dtype_code(x.dtype), stream=stream)
+    _launch(x, "kmip_group_norm_fwd", stream,
+            (x.data_ptr(), _addr(weight), _addr(bias), _addr(graph_offsets), N, C, groups, eps,
+             _act_code(act), y.data_ptr(), mean.data_ptr(), rstd.data_ptr()),
+            (G, dtype_code(x.dtype)))
     return y, mean, rstd
 
 
@@ -430,9 +453,10 @@ def group_norm_bwd(dy, x, weight, bias, mean, rstd, groups: int, act: str = "non
     dw = db = None
     if weight is not None:
         dw, db = torch.empty_like(weight), torch.empty_like(weight)
-    _launch(x, "kmip_group_norm_bwd", _ptr(dy), _ptr(x), _ptr(weight), _ptr(bias),
-            _ptr(graph_offsets), _ptr(mean), _ptr(rstd), N, C, groups, _act_code(act), _ptr(dx),
-            _ptr(dw), _ptr(db), _STREAM, G, dtype_code(x.dtype), stream=stream)
+    _launch(x, "kmip_group_norm_bwd", stream,
+            (dy.data_ptr(), x.data_ptr(), _addr(weight), _addr(bias), _addr(graph_offsets),
+             mean.data_ptr(), rstd.data_ptr(), N, C, groups, _act_code(act), dx.data_ptr(),
+             _addr(dw), _addr(db)), (G, dtype_code(x.dtype)))
     return dx, dw, db
 
 
@@ -452,8 +476,9 @@ def ffn_fwd(x, wg, wu, wd, act: str = "silu", stream=None):
     (kmip_ffn_fwd).  x: [N, C] bf16 or fp32; wg, wu: [F, C]; wd: [C, F]."""
     N, C, F = _ffn_args(x, wg, wu, wd)
     y = torch.empty_like(x)
-    _launch(x, "kmip_ffn_fwd", _ptr(x), _ptr(wg), _ptr(wu), _ptr(wd), N, C, F, _act_code(act),
-            _ptr(y), _STREAM, dtype_code(x.dtype), stream=stream)
+    _launch(x, "kmip_ffn_fwd", stream,
+            (x.data_ptr(), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(), N, C, F, _act_code(act),
+             y.data_ptr()), (dtype_code(x.dtype),))
     return y
 
 
@@ -464,9 +489,10 @@ def ffn_bwd(dy, x, wg, wu, wd, act: str = "silu", stream=None):
     _expect(dy, "dy", (N, C), x.dtype)
     dx = torch.empty_like(x)
     dwg, dwu, dwd = torch.empty_like(wg), torch.empty_like(wu), torch.empty_like(wd)
-    _launch(x, "kmip_ffn_bwd", _ptr(dy), _ptr(x), _ptr(wg), _ptr(wu), _ptr(wd), N, C, F,
-            _act_code(act), _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(dwd), _STREAM,
-            dtype_code(x.dtype), stream=stream)
+    _launch(x, "kmip_ffn_bwd", stream,
+            (dy.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(), N, C, F,
+             _act_code(act), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr()),
+            (dtype_code(x.dtype),))
     return dx, dwg, dwu, dwd
 
 

@@ -2,18 +2,33 @@
 // block, and their derivatives.
 //
 // T is the element type that results are rounded to: for bf16 (half a step is
-// 2^-9 of the value) the exponential is the fast one and the quotient an
-// approximate division, both good to about 2^-21; fp32 takes the accurate ones.
+// 2^-9 to 2^-8 of the value) the exponential and the quotient are the approximate
+// instructions, good to about 2^-21 together: four instructions a sigmoid,
+// where the accurate ones made the feed-forward's epilogue twice as long as
+// its products.  fp32 takes the accurate ones.
 #pragma once
 
 #include "kmip_common.cuh"
 
 namespace kmip {
 
+// 2^x and 1/x by one instruction each, subnormals as zero (2^x = 0 below
+// -126, 1/inf = 0: both what the sigmoid needs).
+__device__ __forceinline__ float ex2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 template <typename T>
 __device__ __forceinline__ float sigmoid(float z) {
   if constexpr (sizeof(T) == 2)
-    return __fdividef(1.f, 1.f + __expf(-z));
+    return rcp_fast(1.f + ex2_fast(-1.4426950408889634f * z));  // log2(e)
   else
     return 1.f / (1.f + expf(-z));
 }
@@ -43,7 +58,7 @@ __device__ __forceinline__ void act_both(float z, float& f, float& g) {
   if constexpr (ACT == KMIP_ACT_SILU) {
     const float s = sigmoid<T>(z);
     f = z * s;
-    g = s * fmaf(z, 1.f - s, 1.f);
+    g = fmaf(f, 1.f - s, s);
   } else if constexpr (ACT == KMIP_ACT_GELU) {
     const float c = gauss_cdf(z);
     f = z * c;

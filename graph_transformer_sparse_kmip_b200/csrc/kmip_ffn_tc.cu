@@ -19,17 +19,20 @@
 // CTAs would read 96 KB; at 8192 flop per cycle and SM a step takes 512
 // cycles, and 64 bytes per cycle and SM is what L2 can feed.  Warp 8 issues
 // TMA loads into a ring of 32 KB stages, warp 9 of the leading CTA issues the
-// MMAs, warps 0-7 of both CTAs read the accumulators (128 lanes each, two
-// warps per quarter, one per half of the columns), compute and hand swizzled
-// boxes to TMA stores.  Accumulators are double-buffered; the backward's
-// three need 384 of 512 columns, so there dh alone has two buffers, and dh of
-// the next tile runs while a and b are read.
+// MMAs, warps 0-15 of both CTAs read the accumulators (a quarter of the lanes
+// and of the columns each), compute, and hand boxes of 32 rows by 32 columns
+// to TMA stores through a corner of shared memory of their own, so no warp
+// waits for another.  (Stores from registers, 32 bytes a lane, took 2.3
+// cycles a sector: 7,700 cycles for dA, dB, h of a 256 x 128 tile.)
+// Accumulators are double-buffered; the backward's three need 384 of 512
+// columns, so there dh alone has two buffers, and dh of the next tile runs
+// while a and b are read.
 //
 // The weight gradients contract over N: both operands have the contraction
-// index outermost.  They are few tiles and long sums, so the work units
-// (tile, 64 rows) are dealt to the clusters in equal contiguous runs; a tile
-// cut by a run's end leaves fp32 partials that a second kernel adds in the
-// order of the runs: the same bits every time.
+// index outermost.  Tiles that fill all clusters are computed whole, all
+// clusters at the same rows, so that operands come out of L2; the remaining
+// tiles are cut along N into parts, fp32 partial tiles that a second kernel
+// adds in order: the same bits every time.
 #include <cuda.h>
 
 #include "kmip_act.cuh"
@@ -58,20 +61,22 @@ constexpr int kGluF = 128;           // F columns of a GLU tile
 constexpr int kStageA = kHalfM * kBK * 2;   // 16 KB
 constexpr int kStageB = 128 * kBK * 2;      // at most
 constexpr int kStage = kStageA + kStageB;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kThreads = (kEpiWarps + 2) * 32;
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s
 
-constexpr int stages_of(Mode m) { return m == kGluBwd ? 5 : 6; }
-constexpr int staging_of(Mode m) {
-  // a box of 64 columns per half, or three of 32 (dA, dB, h)
-  return m == kGluBwd ? 2 * 3 * kHalfM * 64 : 2 * kHalfM * 128;
+constexpr int kBox = 32 * 32 * 2;    // a warp's output box
+
+constexpr int boxes_of(int mode) { return mode == kGluBwd ? 3 : 1; }
+constexpr int stages_of(int mode) { return mode == kGluBwd ? 4 : 6; }
+constexpr int smem_of(int mode) {
+  return 1024 + stages_of(mode) * kStage + kEpiWarps * boxes_of(mode) * kBox + 256;
 }
-constexpr int smem_of(Mode m) { return 1024 + stages_of(m) * kStage + staging_of(m) + 256; }
 static_assert(smem_of(kGlu) <= 232448 && smem_of(kGluBwd) <= 232448, "shared memory");
 
 struct alignas(64) Maps {
-  CUtensorMap m[8];
+  CUtensorMap m[5];    // operands
+  CUtensorMap out[3];  // kGlu h; kNT, kNN out; kGluBwd dA, dB, h; kTN dWg, dWu
 };
 
 struct GemmParams {
@@ -80,70 +85,54 @@ struct GemmParams {
   int tiles;           // all tiles
   int kb0, kb1;        // steps of the two segments
   int tiles_p;         // kTN: row tiles of one of the three gradients
-  float4* part;        // kTN: partial tiles, two per cluster
-  __nv_bfloat16* dwd;  // kTN: [cols][rows]
+  int whole;           // kTN: tiles computed whole
+  int parts;           // kTN: parts of each of the others
+  float4* part;        // kTN: their partial tiles
+  __nv_bfloat16 *dwg, *dwu, *dwd;  // kTN: [rows][cols] twice, [cols][rows]
   int* status;
 };
 
-// A cluster's share of the work: tiles c, c + clusters, ... or, for kTN, the
-// units [c U / clusters, (c + 1) U / clusters) of U = tiles * kb0.
+// A piece of a cluster's work: steps [k0, k0 + kn) of a tile; slot = the
+// partial tile it goes to, or -1.
 struct Item {
-  int tile, k0, kn;
+  int tile, k0, kn, slot;
 };
 
-__device__ __forceinline__ int64_t run_start(int64_t units, int c, int clusters) {
-  return units * c / clusters;
-}
-
+// Cluster c takes tiles c, c + clusters, ...; kTN: first whole tiles like
+// that, then parts, numbered with the tile running fastest, likewise.
 template <int MODE>
 struct Walk {
-  int64_t u, end;
-  int step, kb;
-  __device__ Walk(const GemmParams& p, int c, int clusters) {
-    kb = p.kb0;
-    if (MODE == kTN) {
-      const int64_t units = (int64_t)p.tiles * kb;
-      u = run_start(units, c, clusters);
-      end = run_start(units, c + 1, clusters);
+  int64_t i;
+  int clusters;
+  __device__ Walk(int c, int n) : i(c), clusters(n) {}
+  __device__ bool next(const GemmParams& p, Item& it) {
+    if (MODE == kTN && i >= p.whole) {
+      const int rest = p.tiles - p.whole;
+      const int64_t j = i - p.whole;
+      if (j >= (int64_t)rest * p.parts) return false;
+      const int s = (int)(j / rest);
+      it.tile = p.whole + (int)(j % rest);
+      it.k0 = (int)((int64_t)p.kb0 * s / p.parts);
+      it.kn = (int)((int64_t)p.kb0 * (s + 1) / p.parts) - it.k0;
+      it.slot = p.parts > 1 ? (int)j : -1;
     } else {
-      u = c;
-      end = p.tiles;
-      step = clusters;
-    }
-  }
-  __device__ bool next(Item& it) {
-    if (u >= end) return false;
-    if (MODE == kTN) {
-      it.tile = (int)(u / kb);
-      it.k0 = (int)(u % kb);
-      const int64_t left = end - u;
-      it.kn = (int)(left < kb - it.k0 ? left : kb - it.k0);
-      u += it.kn;
-    } else {
-      it.tile = (int)u;
+      if (i >= p.tiles) return false;
+      it.tile = (int)i;
       it.k0 = 0;
-      it.kn = kb;
-      u += step;
+      it.kn = p.kb0;
+      it.slot = -1;
     }
+    i += clusters;
     return true;
   }
 };
 
-// 32 packed bf16 pairs of a row into a box of 64 columns (128-byte rows,
-// 128-byte swizzle), columns 32 c ..; or into a box of 32 (64-byte rows).
-__device__ __forceinline__ void put_box64(uint32_t box, int row, int c, const uint32_t (&w)[16]) {
+// 16 packed bf16 columns of a row into a box of 32 (64-byte rows with their
+// swizzle): the left (c = 0) or right half.
+__device__ __forceinline__ void put_box(uint32_t box, int lane, int c, const uint32_t (&w)[8]) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint32_t at = box + row * 128 + (((c * 4 + q) ^ (row & 7)) << 4);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[4 * q]),
-                 "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
-                 : "memory");
-  }
-}
-__device__ __forceinline__ void put_box32(uint32_t box, int row, const uint32_t (&w)[16]) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint32_t at = box + row * 64 + ((q ^ ((row >> 1) & 3)) << 4);
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t at = box + lane * 64 + (((2 * c + q) ^ ((lane >> 1) & 3)) << 4);
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[4 * q]),
                  "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
                  : "memory");
@@ -159,7 +148,7 @@ template <int MODE, int BN, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
   using T = __nv_bfloat16;
-  constexpr int kStages = stages_of((Mode)MODE);
+  constexpr int kStages = stages_of(MODE);
   constexpr int kBufs = MODE == kGluBwd ? 1 : 2;
   constexpr int kBufCols = MODE == kGluBwd ? 0 : BN;
   constexpr int kTmemCols = MODE == kGluBwd ? 512 : 2 * BN;
@@ -167,8 +156,8 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t staging = base + kStages * kStage;
-  const uint32_t bars = staging + staging_of((Mode)MODE);
+  const uint32_t boxes = base + kStages * kStage;
+  const uint32_t bars = boxes + kEpiWarps * boxes_of(MODE) * kBox;
   const uint32_t full = bars, empty = bars + 8 * kStages;
   const uint32_t tfull = empty + 8 * kStages, tempty = tfull + 16;
   __shared__ uint32_t tmem_slot;
@@ -207,10 +196,10 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
     if (lane == 0) {
       const uint32_t full0 = map_to_cta(full, 0);
       uint32_t it_no = 0;
-      Walk<MODE> walk(p, cluster, clusters);
+      Walk<MODE> walk(cluster, clusters);
       Item it;
       bool ok = true;
-      while (ok && walk.next(it)) {
+      while (ok && walk.next(p, it)) {
         const int mt = it.tile / p.tiles_n, nt = it.tile % p.tiles_n;
         for (int seg = 0; seg < kSegs && ok; ++seg) {
           const int kn = seg ? p.kb1 : (MODE == kTN ? it.kn : p.kb0);
@@ -264,10 +253,10 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
     // ----------------------------------------------------------------- MMA
     if (lane == 0 && rank == 0) {
       uint32_t it_no = 0, tile_no = 0;
-      Walk<MODE> walk(p, cluster, clusters);
+      Walk<MODE> walk(cluster, clusters);
       Item it;
       bool ok = true;
-      while (ok && walk.next(it)) {
+      while (ok && walk.next(p, it)) {
         const uint32_t buf = kBufs == 2 ? tile_no & 1 : 0;
         const uint32_t use = kBufs == 2 ? tile_no >> 1 : tile_no;
         if (MODE != kGluBwd) {
@@ -321,163 +310,141 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const bool issuer = (threadIdx.x & 127) == 0;
-    const uint32_t box = staging + half * (staging_of((Mode)MODE) / 2);
     const uint32_t tempty0 = map_to_cta(tempty, 0);
+    const uint32_t box = boxes + warp * boxes_of(MODE) * kBox;
+    // The warp's boxes are free again / filled and on their way out.
+    auto boxes_free = [&] {
+      if (lane == 0) bulk_wait_read();
+      __syncwarp();
+    };
+    auto send = [&](int n, int first, int x, int y) {
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0 && y < p.rows && x < p.cols) {
+        for (int i = 0; i < n; ++i) tma_store_2d(&maps.out[first + i], box + i * kBox, x, y);
+        bulk_commit();
+      }
+    };
     uint32_t tile_no = 0;
-    Walk<MODE> walk(p, cluster, clusters);
+    Walk<MODE> walk(cluster, clusters);
     Item it;
-    while (walk.next(it)) {
+    while (walk.next(p, it)) {
       const int mt = it.tile / p.tiles_n, nt = it.tile % p.tiles_n;
       const uint32_t buf = kBufs == 2 ? tile_no & 1 : 0;
       const uint32_t use = kBufs == 2 ? tile_no >> 1 : tile_no;
-      // the half's four warps go on or give up together (they meet at barriers)
-      if (!named_all(1 + half, 128, mbar_wait(tfull + 8 * buf, use & 1, abort_flag, kTimeoutNs)))
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(tfull + 8 * buf, use & 1, abort_flag, kTimeoutNs)))
         break;
       tc_fence_after();
       const uint32_t acc = lanes + buf * kBufCols;
-      const int m0 = mt * kTileM + rank * kHalfM;
-
-      // This thread has read what it needs of the accumulators.
+      // This warp has read what it needs of the accumulators.
       auto release = [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * buf);
       };
-      // The half's staging is free again / complete and on its way out.
-      auto staging_free = [&] {
-        if (issuer) bulk_wait_read();
-        named_sync(1 + half, 128);
-      };
+      const int m0 = (MODE == kTN ? mt % p.tiles_p : mt) * kTileM + (int)rank * kHalfM +
+                     (warp & 3) * 32;
 
       if constexpr (MODE == kGlu) {
-        const int f0 = nt * kGluF + half * 64;
-        uint32_t w[2][16];
-#pragma unroll
+        const int f0 = nt * kGluF + quarter * 32;
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
-          float g[32], u[32];
-          tmem_ld32(acc + half * 64 + c * 32, g);
-          tmem_ld32(acc + 128 + half * 64 + c * 32, u);
+          const int col = quarter * 32 + c * 16;
+          float g[16], u[16];
+          tmem_ld16(acc + col, g);
+          tmem_ld16(acc + kGluF + col, u);
           tmem_ld_wait_all();
           reg_fence(g);
           reg_fence(u);
           if (c == 1) release();
+          uint32_t w[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w[c][e] = pack2(act_value<T, ACT>(g[2 * e]) * u[2 * e],
-                            act_value<T, ACT>(g[2 * e + 1]) * u[2 * e + 1]);
+          for (int e = 0; e < 8; ++e)
+            w[e] = pack2(act_value<T, ACT>(g[2 * e]) * u[2 * e],
+                         act_value<T, ACT>(g[2 * e + 1]) * u[2 * e + 1]);
+          if (c == 0) boxes_free();
+          put_box(box, lane, c, w);
         }
-        staging_free();
-        put_box64(box, row, 0, w[0]);
-        put_box64(box, row, 1, w[1]);
-        fence_async_shared();
-        named_sync(1 + half, 128);
-        if (issuer && m0 < p.rows && f0 < p.cols) {
-          tma_store_2d(&maps.m[3], box, f0, m0);
-          bulk_commit();
-        }
+        send(1, 0, f0, m0);
       } else if constexpr (MODE == kGluBwd) {
-        const uint32_t acc_dh = lanes + 256 + (tile_no & 1) * 128;
+        const uint32_t acc_dh = lanes + 2 * kGluF + (tile_no & 1) * kGluF;
+        const int f0 = nt * kGluF + quarter * 32;
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
-          const int col = half * 64 + c * 32, f0 = nt * kGluF + col;
-          float a[32], b[32], dh[32];
-          tmem_ld32(acc + col, a);
-          tmem_ld32(acc + 128 + col, b);
-          tmem_ld32(acc_dh + col, dh);
+          const int col = quarter * 32 + c * 16;
+          float a[16], b[16], dh[16];
+          tmem_ld16(acc + col, a);
+          tmem_ld16(acc + kGluF + col, b);
+          tmem_ld16(acc_dh + col, dh);
           tmem_ld_wait_all();
           reg_fence(a);
           reg_fence(b);
           reg_fence(dh);
           if (c == 1) release();
-          uint32_t wa[16], wb[16], wh[16];
+          uint32_t wa[8], wb[8], wh[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < 8; ++e) {
             float ra[2], rb[2], rh[2];
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-              float f, g;
-              act_both<T, ACT>(a[2 * e + z], f, g);
-              ra[z] = dh[2 * e + z] * b[2 * e + z] * g;
-              rb[z] = dh[2 * e + z] * f;
-              rh[z] = f * b[2 * e + z];
+              float fa, ga;
+              act_both<T, ACT>(a[2 * e + z], fa, ga);
+              ra[z] = dh[2 * e + z] * b[2 * e + z] * ga;
+              rb[z] = dh[2 * e + z] * fa;
+              rh[z] = fa * b[2 * e + z];
             }
             wa[e] = pack2(ra[0], ra[1]);
             wb[e] = pack2(rb[0], rb[1]);
             wh[e] = pack2(rh[0], rh[1]);
           }
-          staging_free();
-          put_box32(box, row, wa);
-          put_box32(box + 8192, row, wb);
-          put_box32(box + 16384, row, wh);
-          fence_async_shared();
-          named_sync(1 + half, 128);
-          if (issuer && m0 < p.rows && f0 < p.cols) {
-            tma_store_2d(&maps.m[5], box, f0, m0);
-            tma_store_2d(&maps.m[6], box + 8192, f0, m0);
-            tma_store_2d(&maps.m[7], box + 16384, f0, m0);
-            bulk_commit();
-          }
+          if (c == 0) boxes_free();
+          put_box(box, lane, c, wa);
+          put_box(box + kBox, lane, c, wb);
+          put_box(box + 2 * kBox, lane, c, wh);
         }
+        send(3, 0, f0, m0);
       } else {
-        const bool partial = MODE == kTN && it.kn < p.kb0;
         const int prob = MODE == kTN ? mt / p.tiles_p : 0;
-        const int r0 = MODE == kTN ? (mt % p.tiles_p) * kTileM + (int)rank * kHalfM : m0;
-        // this cluster's first run starts inside the tile: slot 0; its last
-        // one ends inside: slot 1
-        float4* part = MODE == kTN
-                           ? p.part + ((int64_t)(2 * cluster + (it.k0 == 0)) * 2 + rank) *
-                                          (BN / 4 * kHalfM)
-                           : nullptr;
+        float4* part =
+            MODE == kTN ? p.part + ((int64_t)it.slot * 2 + rank) * (BN / 4 * kHalfM) : nullptr;
 #pragma unroll 1
         for (int j = 0; j < BN / 128; ++j) {
-          const int col = half * (BN / 2) + j * 64, c0 = nt * BN + col;
-          float v[2][32];
-          tmem_ld32(acc + col, v[0]);
-          tmem_ld32(acc + col + 32, v[1]);
+          const int col = quarter * (BN / 4) + j * 32, n = nt * BN + col;
+          float v[32];
+          tmem_ld32(acc + col, v);
           tmem_ld_wait_all();
-          reg_fence(v[0]);
-          reg_fence(v[1]);
+          reg_fence(v);
           if (j == BN / 128 - 1) release();
-          if (partial) {
+          if (MODE == kTN && it.slot >= 0) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 8; ++e)
               part[(int64_t)(col / 4 + e) * kHalfM + row] =
-                  make_float4(v[e / 8][4 * (e % 8)], v[e / 8][4 * (e % 8) + 1],
-                              v[e / 8][4 * (e % 8) + 2], v[e / 8][4 * (e % 8) + 3]);
+                  make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
           } else if (MODE == kTN && prob == 2) {
             // dWd is [C][F]: neighbouring lanes hold neighbouring F
-            if (r0 + row < p.rows) {
+            if (m0 + lane < p.rows) {
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (c0 + e < p.cols)
-                  p.dwd[(int64_t)(c0 + e) * p.rows + r0 + row] =
-                      __float2bfloat16_rn(v[e / 32][e % 32]);
+              for (int e = 0; e < 32; ++e)
+                if (n + e < p.cols)
+                  p.dwd[(int64_t)(n + e) * p.rows + m0 + lane] = __float2bfloat16_rn(v[e]);
             }
           } else {
-            uint32_t w[2][16];
+            uint32_t w[2][8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              w[0][e] = pack2(v[0][2 * e], v[0][2 * e + 1]);
-              w[1][e] = pack2(v[1][2 * e], v[1][2 * e + 1]);
-            }
-            staging_free();
-            put_box64(box, row, 0, w[0]);
-            put_box64(box, row, 1, w[1]);
-            fence_async_shared();
-            named_sync(1 + half, 128);
-            if (issuer && r0 < p.rows && c0 < p.cols) {
-              tma_store_2d(&maps.m[MODE == kTN ? 5 + prob : 4], box, c0, r0);
-              bulk_commit();
-            }
+            for (int e = 0; e < 16; ++e) w[e / 8][e % 8] = pack2(v[2 * e], v[2 * e + 1]);
+            boxes_free();
+            put_box(box, lane, 0, w[0]);
+            put_box(box, lane, 1, w[1]);
+            send(1, prob, n, m0);
           }
         }
       }
       ++tile_no;
     }
-    if (issuer) bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
   }
 
   // ------------------------------------------------------------- teardown
@@ -493,31 +460,21 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
   }
 }
 
-// Adds the partial tiles of the weight gradients in the order of the runs.
-// Grid: (tile, CTA of the pair, 32-column group); 128 threads, one per row.
+// Adds the partial tiles of the weight gradients in order.  Grid: (tile that
+// was cut, CTA of the pair, 8-column group); 128 threads, one per row.
 template <int BN>
-__global__ void __launch_bounds__(128) ffn_join_kernel(const GemmParams p, int clusters,
-                                                       __nv_bfloat16* dwg, __nv_bfloat16* dwu) {
-  const int tile = blockIdx.x, rank = blockIdx.y, row = threadIdx.x;
-  const int64_t units = (int64_t)p.tiles * p.kb0, u0 = (int64_t)tile * p.kb0, u1 = u0 + p.kb0;
-  // the cluster whose run holds unit u0
-  int c = (int)(u0 * clusters / units);
-  while (run_start(units, c + 1, clusters) <= u0) ++c;
-  while (run_start(units, c, clusters) > u0) --c;
-  if (run_start(units, c, clusters) <= u0 && run_start(units, c + 1, clusters) >= u1)
-    return;  // written whole by its cluster
-  float4 v[8];
+__global__ void __launch_bounds__(128) ffn_join_kernel(const GemmParams p) {
+  const int rest = p.tiles - p.whole, tile = p.whole + blockIdx.x, rank = blockIdx.y;
+  const int row = threadIdx.x;
+  float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  const float4* src = p.part + ((int64_t)blockIdx.x * 2 + rank) * (BN / 4 * kHalfM) +
+                      (int64_t)blockIdx.z * 2 * kHalfM + row;
+  const int64_t step = (int64_t)rest * 2 * (BN / 4 * kHalfM);
+#pragma unroll 4
+  for (int s = 0; s < p.parts; ++s, src += step) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (; c < clusters && run_start(units, c, clusters) < u1; ++c) {
-    const int64_t start = run_start(units, c, clusters);
-    if (run_start(units, c + 1, clusters) == start) continue;  // empty run
-    const float4* src = p.part +
-                        ((int64_t)(2 * c + (start <= u0)) * 2 + rank) * (BN / 4 * kHalfM) +
-                        (int64_t)blockIdx.z * 8 * kHalfM + row;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float4 t = src[(int64_t)e * kHalfM];
+    for (int e = 0; e < 2; ++e) {
+      const float4 t = src[e * kHalfM];
       v[e].x += t.x;
       v[e].y += t.y;
       v[e].z += t.z;
@@ -526,21 +483,17 @@ __global__ void __launch_bounds__(128) ffn_join_kernel(const GemmParams p, int c
   }
   const int mt = tile / p.tiles_n, nt = tile % p.tiles_n, prob = mt / p.tiles_p;
   const int r = (mt % p.tiles_p) * kTileM + rank * kHalfM + row;
-  const int c0 = nt * BN + blockIdx.z * 32;
-  if (r >= p.rows) return;
+  const int c = nt * BN + blockIdx.z * 8;
+  if (r >= p.rows || c >= p.cols) return;  // cols is a multiple of 8
+  if (prob == 2) {
+    const float f[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int col = c0 + 4 * e;  // cols is a multiple of 8
-    if (col >= p.cols) break;
-    if (prob == 2) {
-      p.dwd[(int64_t)col * p.rows + r] = __float2bfloat16_rn(v[e].x);
-      p.dwd[(int64_t)(col + 1) * p.rows + r] = __float2bfloat16_rn(v[e].y);
-      p.dwd[(int64_t)(col + 2) * p.rows + r] = __float2bfloat16_rn(v[e].z);
-      p.dwd[(int64_t)(col + 3) * p.rows + r] = __float2bfloat16_rn(v[e].w);
-    } else {
-      *reinterpret_cast<uint2*>((prob ? dwu : dwg) + (int64_t)r * p.cols + col) =
-          make_uint2(pack2(v[e].x, v[e].y), pack2(v[e].z, v[e].w));
-    }
+    for (int e = 0; e < 8; ++e)
+      p.dwd[(int64_t)(c + e) * p.rows + r] = __float2bfloat16_rn(f[e]);
+  } else {
+    *reinterpret_cast<uint4*>((prob ? p.dwu : p.dwg) + (int64_t)r * p.cols + c) =
+        make_uint4(pack2(v[0].x, v[0].y), pack2(v[0].z, v[0].w), pack2(v[1].x, v[1].y),
+                   pack2(v[1].z, v[1].w));
   }
 }
 
@@ -554,10 +507,10 @@ int clusters_for(int64_t tiles) {
 template <int MODE, int BN, int ACT>
 cudaError_t launch_gemm(const Maps& maps, const GemmParams& p, int clusters, cudaStream_t stream) {
   auto kern = ffn_gemm_kernel<MODE, BN, ACT>;
-  constexpr int smem = smem_of((Mode)MODE);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       smem_of(MODE));
   if (e != cudaSuccess) return e;
-  kern<<<2 * clusters, kThreads, smem, stream>>>(maps, p);
+  kern<<<2 * clusters, kThreads, smem_of(MODE), stream>>>(maps, p);
   return cudaGetLastError();
 }
 
@@ -580,21 +533,30 @@ int tile_cols(int cols) {
   return ceil_div(cols, 256) * 256 * 4 >= ceil_div(cols, 128) * 128 * 5 ? 128 : 256;
 }
 
+// Output of rows x cols in tiles of kTileM x bn, a contraction of length k.
+GemmParams params(const FfnArgs& a, int rows, int cols, int bn, int k) {
+  GemmParams p{};
+  p.rows = rows;
+  p.cols = cols;
+  p.tiles_n = ceil_div(cols, bn);
+  p.tiles = ceil_div(rows, kTileM) * p.tiles_n;
+  p.kb0 = p.kb1 = ceil_div(k, kBK);
+  p.status = a.status;
+  return p;
+}
+
+bool out_map(CUtensorMap* m, const void* ptr, int rows, int cols) {
+  return encode_map_2d(m, ptr, rows, cols, 32, 32);
+}
+
 }  // namespace
 
 cudaError_t launch_ffn_glu(const FfnArgs& a, void* h, cudaStream_t stream) {
   Maps m;
-  GemmParams p{};
-  p.rows = a.N;
-  p.cols = a.F;
-  p.tiles_n = ceil_div(a.F, kGluF);
-  p.tiles = ceil_div(a.N, kTileM) * p.tiles_n;
-  p.kb0 = ceil_div(a.C, kBK);
-  p.status = a.status;
+  const GemmParams p = params(a, a.N, a.F, kGluF, a.C);
   if (!encode_map_2d(&m.m[0], a.x, a.N, a.C, 64, kHalfM) ||
       !encode_map_2d(&m.m[1], a.wg, a.F, a.C, 64, kGluF) ||
-      !encode_map_2d(&m.m[2], a.wu, a.F, a.C, 64, kGluF) ||
-      !encode_map_2d(&m.m[3], h, a.N, a.F, 64, kHalfM))
+      !encode_map_2d(&m.m[2], a.wu, a.F, a.C, 64, kGluF) || !out_map(&m.out[0], h, a.N, a.F))
     return cudaErrorInvalidValue;
   return launch_act<kGlu>(a.act, m, p, stream);
 }
@@ -602,16 +564,9 @@ cudaError_t launch_ffn_glu(const FfnArgs& a, void* h, cudaStream_t stream) {
 cudaError_t launch_ffn_down(const FfnArgs& a, const void* h, void* y, cudaStream_t stream) {
   Maps m;
   const int bn = tile_cols(a.C);
-  GemmParams p{};
-  p.rows = a.N;
-  p.cols = a.C;
-  p.tiles_n = ceil_div(a.C, bn);
-  p.tiles = ceil_div(a.N, kTileM) * p.tiles_n;
-  p.kb0 = ceil_div(a.F, kBK);
-  p.status = a.status;
+  const GemmParams p = params(a, a.N, a.C, bn, a.F);
   if (!encode_map_2d(&m.m[0], h, a.N, a.F, 64, kHalfM) ||
-      !encode_map_2d(&m.m[1], a.wd, a.C, a.F, 64, bn / 2) ||
-      !encode_map_2d(&m.m[4], y, a.N, a.C, 64, kHalfM))
+      !encode_map_2d(&m.m[1], a.wd, a.C, a.F, 64, bn / 2) || !out_map(&m.out[0], y, a.N, a.C))
     return cudaErrorInvalidValue;
   const int c = clusters_for(p.tiles);
   return bn == 256 ? launch_gemm<kNT, 256, 0>(m, p, c, stream)
@@ -621,21 +576,13 @@ cudaError_t launch_ffn_down(const FfnArgs& a, const void* h, void* y, cudaStream
 cudaError_t launch_ffn_glu_bwd(const FfnArgs& a, const void* dy, void* da, void* db, void* h,
                                cudaStream_t stream) {
   Maps m;
-  GemmParams p{};
-  p.rows = a.N;
-  p.cols = a.F;
-  p.tiles_n = ceil_div(a.F, kGluF);
-  p.tiles = ceil_div(a.N, kTileM) * p.tiles_n;
-  p.kb0 = p.kb1 = ceil_div(a.C, kBK);
-  p.status = a.status;
+  const GemmParams p = params(a, a.N, a.F, kGluF, a.C);
   if (!encode_map_2d(&m.m[0], dy, a.N, a.C, 64, kHalfM) ||
       !encode_map_2d(&m.m[1], a.wd, a.C, a.F, 64, kBK) ||
       !encode_map_2d(&m.m[2], a.x, a.N, a.C, 64, kHalfM) ||
       !encode_map_2d(&m.m[3], a.wg, a.F, a.C, 64, kGluF) ||
-      !encode_map_2d(&m.m[4], a.wu, a.F, a.C, 64, kGluF) ||
-      !encode_map_2d(&m.m[5], da, a.N, a.F, 32, kHalfM) ||
-      !encode_map_2d(&m.m[6], db, a.N, a.F, 32, kHalfM) ||
-      !encode_map_2d(&m.m[7], h, a.N, a.F, 32, kHalfM))
+      !encode_map_2d(&m.m[4], a.wu, a.F, a.C, 64, kGluF) || !out_map(&m.out[0], da, a.N, a.F) ||
+      !out_map(&m.out[1], db, a.N, a.F) || !out_map(&m.out[2], h, a.N, a.F))
     return cudaErrorInvalidValue;
   return launch_act<kGluBwd>(a.act, m, p, stream);
 }
@@ -644,44 +591,56 @@ cudaError_t launch_ffn_dx(const FfnArgs& a, const void* da, const void* db, void
                           cudaStream_t stream) {
   Maps m;
   const int bn = tile_cols(a.C);
-  GemmParams p{};
-  p.rows = a.N;
-  p.cols = a.C;
-  p.tiles_n = ceil_div(a.C, bn);
-  p.tiles = ceil_div(a.N, kTileM) * p.tiles_n;
-  p.kb0 = p.kb1 = ceil_div(a.F, kBK);
-  p.status = a.status;
+  const GemmParams p = params(a, a.N, a.C, bn, a.F);
   if (!encode_map_2d(&m.m[0], da, a.N, a.F, 64, kHalfM) ||
       !encode_map_2d(&m.m[1], db, a.N, a.F, 64, kHalfM) ||
       !encode_map_2d(&m.m[2], a.wg, a.F, a.C, 64, kBK) ||
-      !encode_map_2d(&m.m[3], a.wu, a.F, a.C, 64, kBK) ||
-      !encode_map_2d(&m.m[4], dx, a.N, a.C, 64, kHalfM))
+      !encode_map_2d(&m.m[3], a.wu, a.F, a.C, 64, kBK) || !out_map(&m.out[0], dx, a.N, a.C))
     return cudaErrorInvalidValue;
   const int c = clusters_for(p.tiles);
   return bn == 256 ? launch_gemm<kNN, 256, 0>(m, p, c, stream)
                    : launch_gemm<kNN, 128, 0>(m, p, c, stream);
 }
 
-// Clusters and partial-tile bytes of the weight gradients.
 namespace {
-void wgrad_plan(const FfnArgs& a, int bn, GemmParams& p, int& clusters) {
-  p.rows = a.F;
-  p.cols = a.C;
-  p.tiles_n = ceil_div(a.C, bn);
+
+// Steps of 64 rows that a part costs beside its products (its first loads,
+// its partial tile written and read again).
+constexpr int kPartCost = 8;
+
+// Whole tiles and parts of the weight gradients.
+GemmParams wgrad_params(const FfnArgs& a, int bn, void* dwg, void* dwu, void* dwd) {
+  GemmParams p = params(a, a.F, a.C, bn, a.N);
+  p.dwg = static_cast<__nv_bfloat16*>(dwg);
+  p.dwu = static_cast<__nv_bfloat16*>(dwu);
+  p.dwd = static_cast<__nv_bfloat16*>(dwd);
   p.tiles_p = ceil_div(a.F, kTileM);
-  p.tiles = 3 * p.tiles_p * p.tiles_n;
-  p.kb0 = ceil_div(a.N, kBK);
-  clusters = clusters_for((int64_t)p.tiles * p.kb0);
-  p.status = a.status;
+  p.tiles *= 3;
+  const int all = device_sm_count() / 2;
+  p.whole = p.tiles / all * all;
+  const int rest = p.tiles - p.whole;
+  p.parts = 1;
+  if (rest) {
+    // the number of parts whose last round of clusters idles least
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= p.kb0 && (int64_t)rest * s <= 4 * all; ++s) {
+      const int64_t cost = (int64_t)ceil_div((int64_t)rest * s, all) *
+                           (ceil_div(p.kb0, s) + (s > 1 ? kPartCost : 0));
+      if (cost < best) {
+        best = cost;
+        p.parts = s;
+      }
+    }
+  }
+  return p;
 }
+
 }  // namespace
 
 size_t ffn_wgrad_scratch(const FfnArgs& a) {
   const int bn = tile_cols(a.C);
-  GemmParams p{};
-  int clusters;
-  wgrad_plan(a, bn, p, clusters);
-  return (size_t)clusters * 2 * kTileM * bn * sizeof(float);
+  const GemmParams p = wgrad_params(a, bn, nullptr, nullptr, nullptr);
+  return p.parts > 1 ? (size_t)(p.tiles - p.whole) * p.parts * kTileM * bn * sizeof(float) : 0;
 }
 
 cudaError_t launch_ffn_wgrad(const FfnArgs& a, const void* dy, const void* da, const void* db,
@@ -689,28 +648,25 @@ cudaError_t launch_ffn_wgrad(const FfnArgs& a, const void* dy, const void* da, c
                              cudaStream_t stream) {
   Maps m;
   const int bn = tile_cols(a.C);
-  GemmParams p{};
-  int c;
-  wgrad_plan(a, bn, p, c);
+  GemmParams p = wgrad_params(a, bn, dwg, dwu, dwd);
   p.part = static_cast<float4*>(scratch);
-  p.dwd = static_cast<__nv_bfloat16*>(dwd);
   if (!encode_map_2d(&m.m[0], da, a.N, a.F, 64, kBK) ||
       !encode_map_2d(&m.m[1], db, a.N, a.F, 64, kBK) ||
       !encode_map_2d(&m.m[2], h, a.N, a.F, 64, kBK) ||
       !encode_map_2d(&m.m[3], a.x, a.N, a.C, 64, kBK) ||
-      !encode_map_2d(&m.m[4], dy, a.N, a.C, 64, kBK) ||
-      !encode_map_2d(&m.m[5], dwg, a.F, a.C, 64, kHalfM) ||
-      !encode_map_2d(&m.m[6], dwu, a.F, a.C, 64, kHalfM))
+      !encode_map_2d(&m.m[4], dy, a.N, a.C, 64, kBK) || !out_map(&m.out[0], dwg, a.F, a.C) ||
+      !out_map(&m.out[1], dwu, a.F, a.C))
     return cudaErrorInvalidValue;
+  const int rest = p.tiles - p.whole;
+  const int c = clusters_for(p.whole + (int64_t)rest * p.parts);
   cudaError_t e = bn == 256 ? launch_gemm<kTN, 256, 0>(m, p, c, stream)
                             : launch_gemm<kTN, 128, 0>(m, p, c, stream);
-  if (e != cudaSuccess) return e;
-  const dim3 grid(p.tiles, 2, bn / 32);
-  __nv_bfloat16 *g = static_cast<__nv_bfloat16*>(dwg), *u = static_cast<__nv_bfloat16*>(dwu);
+  if (e != cudaSuccess || p.parts == 1) return e;
+  const dim3 grid(rest, 2, bn / 8);
   if (bn == 256)
-    ffn_join_kernel<256><<<grid, 128, 0, stream>>>(p, c, g, u);
+    ffn_join_kernel<256><<<grid, 128, 0, stream>>>(p);
   else
-    ffn_join_kernel<128><<<grid, 128, 0, stream>>>(p, c, g, u);
+    ffn_join_kernel<128><<<grid, 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
