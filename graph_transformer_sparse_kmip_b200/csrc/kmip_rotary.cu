@@ -10,20 +10,28 @@
 // Angles: the product is taken in fp64 in units of one revolution and reduced
 // to [-1/2, 1/2] there, so that far positions keep their angle (an fp32
 // product of 2e5 rad is off by 8e-3 rad); the reduced angle is rounded to fp32
-// (off by at most 2^-25 revolutions) and goes through sincospif.
+// (off by at most 2^-25 revolutions).  Its sine and cosine: sincospif for
+// fp32 outputs; for bf16, whose half step is 2^-9 or more of the value, the
+// fast ones (2^-20 of the pair in [-pi, pi]) in a fifth of the instructions.
 //
 // Bound: HBM traffic, one read and one write of x.  The angles of a node are
 // the same for all of its heads: a block computes those of its nodes once
 // into shared memory while its loads of x are in flight, so the sine and
-// cosine cost 1 / H of a per-element evaluation.
+// cosine cost 1 / H of a per-element evaluation.  Blocks stay and walk over
+// tiles of nodes, because what a thread does inside a tile (which node, head
+// and elements, which angles: three divisions) is the same for every tile.
 #include "kmip_internal.h"
 
 namespace kmip {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;         // units in flight per thread
-constexpr int kMaxTable = 2048;   // cos/sin pairs a block keeps (16 KiB)
+constexpr int kBlocksPerSm = 4;
+constexpr int kEvals = 2;                     // angles of a thread per tile
+constexpr int kMaxTable = kEvals * kThreads;  // cos/sin pairs of a tile
+
+// Units of a thread per tile: 64 bytes of x in flight either way.
+constexpr int batch_of(bool inter) { return inter ? 4 : 2; }
 
 struct RotaryParams {
   const void* x;
@@ -34,8 +42,9 @@ struct RotaryParams {
   const int32_t* axis;
   int64_t N;
   int H, d, pairs, axes;
-  int nodes;        // nodes per block
+  int nodes;        // nodes per tile
   int chunks;       // units per head
+  int64_t tiles;
   int interleaved;
   float sign;       // -1: inverse rotation
   int copy_tail;    // 0: in place, elements behind the pairs stay
@@ -50,106 +59,173 @@ template <> struct Raw<8> { using type = uint2; };
 template <> struct Raw<4> { using type = uint32_t; };
 template <> struct Raw<2> { using type = uint16_t; };
 
+__device__ __forceinline__ float2 turned(float a, float b, float2 cs) {
+  return make_float2(fmaf(a, cs.x, -b * cs.y), fmaf(a, cs.y, b * cs.x));
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 template <typename T, int V>
 struct Pack {
   using R = typename Raw<sizeof(T) * V>::type;
   union {
     R raw;
     T e[V];
+    uint32_t w[sizeof(T) * V < 4 ? 1 : sizeof(T) * V / 4];
   };
   __device__ Pack() {}
   __device__ void load(const T* p) { raw = *reinterpret_cast<const R*>(p); }
   __device__ void store(T* p) const { *reinterpret_cast<R*>(p) = raw; }
+
+  // Adjacent elements are the pairs; the first n of them turn.
+  __device__ void turn_inside(const float2* cs, int n) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      if (i >= n) break;
+      if constexpr (sizeof(T) == 4) {
+        const float2 r = turned(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]), cs[i]);
+        w[2 * i] = __float_as_uint(r.x);
+        w[2 * i + 1] = __float_as_uint(r.y);
+      } else {
+        const float2 r = turned(low(w[i]), high(w[i]), cs[i]);
+        w[i] = pack(r.x, r.y);
+      }
+    }
+  }
+  // Element i here and in `o` are a pair.
+  __device__ void turn_with(Pack& o, const float2* cs) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float2 r = turned(__uint_as_float(w[i]), __uint_as_float(o.w[i]), cs[i]);
+        w[i] = __float_as_uint(r.x);
+        o.w[i] = __float_as_uint(r.y);
+      }
+    } else if constexpr (V == 1) {
+      const float2 r = turned(__bfloat162float(e[0]), __bfloat162float(o.e[0]), cs[0]);
+      e[0] = __float2bfloat16_rn(r.x);
+      o.e[0] = __float2bfloat16_rn(r.y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const float2 r = turned(low(w[i]), low(o.w[i]), cs[2 * i]);
+        const float2 q = turned(high(w[i]), high(o.w[i]), cs[2 * i + 1]);
+        w[i] = pack(r.x, q.x);
+        o.w[i] = pack(r.y, q.y);
+      }
+    }
+  }
 };
 
-__device__ __forceinline__ float widen(float v) { return v; }
-__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void narrow(float& d, float v) { d = v; }
-__device__ __forceinline__ void narrow(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
-
+// (cos, sin) of an angle in revolutions.
 template <typename T>
-__device__ __forceinline__ void turn(T& u, T& v, float2 cs) {
-  const float a = widen(u), b = widen(v);
-  narrow(u, fmaf(a, cs.x, -b * cs.y));
-  narrow(v, fmaf(a, cs.y, b * cs.x));
+__device__ __forceinline__ float2 unit_circle(double rev) {
+  const float r = (float)(rev - rint(rev));
+  float2 cs;
+  if constexpr (sizeof(T) == 4)
+    sincospif(2.f * r, &cs.y, &cs.x);
+  else
+    __sincosf(6.2831853071795865f * r, &cs.y, &cs.x);
+  return cs;
 }
 
 // A unit is what one thread turns at a time: with halves, V pairs (p, p + P)
-// or V elements behind them; interleaved, V elements (V / 2 pairs).
+// or V elements behind them; interleaved, V elements (V / 2 pairs).  A tile is
+// p.nodes nodes with all their units, or (grid.y) a slice of one node's units.
 template <typename T, int V, typename PosT, bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
-  extern __shared__ float2 table[];  // [nodes][pairs]
-  const int64_t n0 = (int64_t)blockIdx.x * p.nodes;
-  const int nodes = (int)min((int64_t)p.nodes, p.N - n0);
-  const int per_node = p.H * p.chunks;
-  const int units = nodes * per_node;
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) rotary_kernel(const RotaryParams p) {
+  constexpr int kBatch = batch_of(INTER);
+  extern __shared__ float2 tables[];  // [2][nodes][pairs]
   const T* x = static_cast<const T*>(p.x);
   T* out = static_cast<T*>(p.out);
+  const PosT* pos = static_cast<const PosT*>(p.pos);
+  const int per_node = p.H * p.chunks;
   const int rot_chunks = INTER ? p.chunks : p.pairs / V;
-  bool have_table = false;
 
-  for (int base = 0; base < units; base += kBatch * kThreads) {
-    Pack<T, V> a[kBatch], b[kBatch];
-    int at[kBatch];        // (node << 16) | chunk, -1 = none
-    int64_t dst[kBatch];
+  // What this thread does in every tile.
+  uint32_t src[kBatch], dst[kBatch];  // from the tile's first node, in units
+  int node[kBatch], chunk[kBatch];    // node = p.nodes: no unit
 #pragma unroll
-    for (int t = 0; t < kBatch; ++t) {
-      const int i = base + t * kThreads + threadIdx.x;
-      at[t] = -1;
-      if (i < units) {
-        const int node = i / per_node, r = i - node * per_node;
-        const int head = r / p.chunks, c = r - head * p.chunks;
-        const bool pair = c < rot_chunks;
-        if (pair || p.copy_tail) {
-          // tail chunks (halves only) start behind both halves
-          const int e = pair ? c * V : 2 * p.pairs + (c - rot_chunks) * V;
-          const T* src = x + (n0 + node) * p.x_row + head * p.x_head + e;
-          dst[t] = (n0 + node) * p.out_row + head * p.out_head + e;
-          a[t].load(src);
-          if (!INTER && pair) b[t].load(src + p.pairs);
-          at[t] = (node << 16) | c;
-        }
-      }
-    }
-    if (!have_table) {
-      have_table = true;
-      for (int i = threadIdx.x; i < nodes * p.pairs; i += kThreads) {
-        const int node = i / p.pairs, q = i - node * p.pairs;
-        const int ax = p.axis[q];
-        double rev = 0.0;
-        if ((unsigned)ax < (unsigned)p.axes)
-          rev = (double)static_cast<const PosT*>(p.pos)[(n0 + node) * p.axes + ax] *
-                (p.freq[q] * 0.15915494309189535);  // 1 / (2 pi)
-        else
-          record_status(p.status, KMIP_ERR_BAD_INDEX);
-        const float half_turns = (float)(2.0 * (rev - rint(rev)));
-        float2 cs;
-        sincospif(half_turns, &cs.y, &cs.x);
-        cs.y *= p.sign;
-        table[i] = cs;
-      }
-      __syncthreads();
-    }
+  for (int t = 0; t < kBatch; ++t) {
+    const int i = (blockIdx.y * kBatch + t) * kThreads + threadIdx.x;
+    const int n = i / per_node, r = i - n * per_node;
+    const int head = r / p.chunks, c = r - head * p.chunks;
+    const bool pair = c < rot_chunks;
+    node[t] = n < p.nodes && (pair || p.copy_tail) ? n : p.nodes;
+    chunk[t] = c;
+    // tail chunks (halves only) start behind both halves
+    const int e = pair ? c * V : 2 * p.pairs + (c - rot_chunks) * V;
+    src[t] = (uint32_t)((n * p.x_row + head * p.x_head + e) / V);
+    dst[t] = (uint32_t)((n * p.out_row + head * p.out_head + e) / V);
+  }
+  double freq[kEvals];  // revolutions per unit
+  int from[kEvals];     // place of the position in the tile's
+  int last[kEvals];     // node
 #pragma unroll
-    for (int t = 0; t < kBatch; ++t) {
-      if (at[t] < 0) continue;
-      const int c = at[t] & 0xffff;
-      const float2* cs = table + (at[t] >> 16) * p.pairs;
-      if constexpr (INTER) {
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) {
-          const int q = c * (V / 2) + e;
-          if (q < p.pairs) turn(a[t].e[2 * e], a[t].e[2 * e + 1], cs[q]);
-        }
-        a[t].store(out + dst[t]);
+  for (int k = 0; k < kEvals; ++k) {
+    const int i = k * kThreads + threadIdx.x;
+    last[k] = p.nodes;
+    freq[k] = 0.0;
+    from[k] = 0;
+    if (i < p.nodes * p.pairs) {
+      const int n = i / p.pairs, q = i - n * p.pairs;
+      const int ax = p.axis[q];
+      last[k] = n;
+      if ((unsigned)ax < (unsigned)p.axes) {
+        freq[k] = p.freq[q] * 0.15915494309189535;  // 1 / (2 pi)
+        from[k] = n * p.axes + ax;
       } else {
-        if (c < rot_chunks) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) turn(a[t].e[e], b[t].e[e], cs[c * V + e]);
-          b[t].store(out + dst[t] + p.pairs);
-        }
-        a[t].store(out + dst[t]);
+        from[k] = -1;  // its pair stays as it is
+        record_status(p.status, KMIP_ERR_BAD_INDEX);
       }
+    }
+  }
+
+  int buf = 0;
+  for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, buf ^= 1) {
+    const int64_t n0 = tile * p.nodes;
+    const int nodes = (int)min((int64_t)p.nodes, p.N - n0);
+    const T* xt = x + n0 * p.x_row;
+    T* ot = out + n0 * p.out_row;
+    Pack<T, V> a[kBatch], b[kBatch];
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t)
+      if (node[t] < nodes) {
+        a[t].load(xt + (size_t)src[t] * V);
+        if (!INTER && chunk[t] < rot_chunks) b[t].load(xt + (size_t)src[t] * V + p.pairs);
+      }
+    // Two tables in turn: a block-wide barrier per tile keeps a thread from
+    // writing a table that another still reads.
+    float2* table = tables + buf * p.nodes * p.pairs;
+    PosT where[kEvals];
+#pragma unroll
+    for (int k = 0; k < kEvals; ++k)
+      if (last[k] < nodes && from[k] >= 0) where[k] = pos[n0 * p.axes + from[k]];
+#pragma unroll
+    for (int k = 0; k < kEvals; ++k)
+      if (last[k] < nodes) {
+        float2 cs = make_float2(1.f, 0.f);
+        if (from[k] >= 0) cs = unit_circle<T>((double)where[k] * freq[k]);
+        cs.y *= p.sign;
+        table[k * kThreads + threadIdx.x] = cs;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t) {
+      if (node[t] >= nodes) continue;
+      const int c = chunk[t];
+      const float2* cs = table + node[t] * p.pairs;
+      if constexpr (INTER) {
+        a[t].turn_inside(cs + c * (V / 2), p.pairs - c * (V / 2));
+      } else if (c < rot_chunks) {
+        a[t].turn_with(b[t], cs + c * V);
+        b[t].store(ot + (size_t)dst[t] * V + p.pairs);
+      }
+      a[t].store(ot + (size_t)dst[t] * V);
     }
   }
 }
@@ -159,15 +235,36 @@ cudaError_t launch(RotaryParams p, cudaStream_t stream) {
   // interleaved units are V elements; with halves the pairs and the tail
   // each make whole units
   p.chunks = INTER ? p.d / V : p.pairs / V + (p.d - 2 * p.pairs) / V;
-  const int per_node = p.H * p.chunks;
-  int nodes = kBatch * kThreads / per_node;
+  constexpr int kUnits = batch_of(INTER) * kThreads;
+  const int per_node = p.H * p.chunks, sms = device_sm_count();
+  int64_t nodes = kUnits / per_node;
   if (p.pairs && nodes > kMaxTable / p.pairs) nodes = kMaxTable / p.pairs;
-  // few nodes: one per block, so that more SMs share the latency
-  if (nodes > (p.N + 591) / 592) nodes = (int)((p.N + 591) / 592);
-  p.nodes = nodes < 1 ? 1 : nodes;
-  const int64_t blocks = (p.N + p.nodes - 1) / p.nodes;
-  const size_t smem = sizeof(float2) * (size_t)p.nodes * p.pairs;
-  rotary_kernel<T, V, PosT, INTER><<<(unsigned)blocks, kThreads, smem, stream>>>(p);
+  // few nodes: smaller tiles, one for every block that can be resident
+  const int most = kBlocksPerSm * sms;
+  const int64_t share = (p.N + most - 1) / most;
+  if (nodes > share) nodes = share;
+  // a thread's offsets in a tile are held in 32 bits, in units of V elements
+  const int64_t row = p.x_row > p.out_row ? p.x_row : p.out_row;
+  const int64_t head = p.x_head > p.out_head ? p.x_head : p.out_head;
+  auto reach = [&](int64_t n) { return ((n - 1) * row + (p.H - 1) * head + p.d) / V; };
+  if (nodes < 1 || reach(nodes) > UINT32_MAX) nodes = 1;
+  if (reach(1) > UINT32_MAX) {  // heads far apart: one launch for each
+    const int H = p.H;
+    p.H = 1;
+    for (int h = 0; h < H; ++h) {
+      const cudaError_t e = launch<T, V, PosT, INTER>(p, stream);
+      if (e != cudaSuccess) return e;
+      p.x = static_cast<const T*>(p.x) + p.x_head;
+      p.out = static_cast<T*>(p.out) + p.out_head;
+    }
+    return cudaSuccess;
+  }
+  p.nodes = (int)nodes;
+  p.tiles = (p.N + p.nodes - 1) / p.nodes;
+  const size_t smem = 2 * sizeof(float2) * (size_t)p.nodes * p.pairs;
+  const dim3 grid((unsigned)(p.tiles < most ? p.tiles : most),
+                  (unsigned)((per_node + kUnits - 1) / kUnits));
+  rotary_kernel<T, V, PosT, INTER><<<grid, kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
