@@ -322,11 +322,11 @@ def attn_bwd(dOut, Q, K, V, idx, lse, scale: float, stream=None, deterministic=F
 def _same_device(x, *ts):
     """Every tensor on x's CUDA device and contiguous (x itself may be
     strided)."""
-    if not x.is_cuda:
-        raise ValueError("libkmip takes CUDA tensors")
     dev = x.get_device()
+    if dev < 0:
+        raise ValueError("libkmip takes CUDA tensors")
     for t in ts:
-        if t is not None and (not t.is_cuda or t.get_device() != dev or not t.is_contiguous()):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             raise ValueError(f"expected a contiguous tensor on {x.device}")
 
 
@@ -345,9 +345,10 @@ def _offsets(graph_offsets):
     """Checks graph_offsets (int32 [G+1] or None); returns G."""
     if graph_offsets is None:
         return 1
-    if graph_offsets.dtype != torch.int32 or graph_offsets.dim() != 1 or graph_offsets.numel() < 2:
+    shape = graph_offsets.shape
+    if graph_offsets.dtype != torch.int32 or len(shape) != 1 or shape[0] < 2:
         raise ValueError("graph_offsets: expected int32 [G + 1] with G >= 1")
-    return graph_offsets.numel() - 1
+    return shape[0] - 1
 
 
 def _addr(t):
@@ -355,6 +356,7 @@ def _addr(t):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch(x, name, stream, args, tail):
@@ -362,7 +364,7 @@ def _launch(x, name, stream, args, tail):
     device current: on `stream`, or on that device's current stream.  Raises
     on a status."""
     dev = x.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         with torch.cuda.device(dev):
             return _launch(x, name, stream, args, tail)
     if stream is not None:
@@ -371,7 +373,7 @@ def _launch(x, name, stream, args, tail):
         s = _raw_stream(dev)
     else:
         s = torch.cuda.current_stream().cuda_stream
-    rc = _call(name, *args, s, *tail)
+    rc = _call(name, *args, s, *tail) if _NVTX else getattr(_lib or load(), name)(*args, s, *tail)
     if rc:
         raise KmipError(rc, name)
 
@@ -426,7 +428,7 @@ def group_norm_fwd(x, weight, bias, groups: int, eps: float = 1e-5, act: str = "
     _expect(weight, "weight", (C,), x.dtype)
     _expect(bias, "bias", (C,), x.dtype)
     y = torch.empty_like(x)
-    mean = torch.empty((G, groups), dtype=torch.float32, device=x.device)
+    mean = x.new_empty((G, groups), dtype=torch.float32)
     rstd = torch.empty_like(mean)
     _launch(x, "kmip_group_norm_fwd", stream,
             (x.data_ptr(), _addr(weight), _addr(bias), _addr(graph_offsets), N, C, groups, eps,

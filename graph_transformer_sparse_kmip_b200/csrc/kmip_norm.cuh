@@ -1,0 +1,543 @@
+// kmip_norm.cuh -- group norm per graph with an activation, channels last: what
+// its kernels share (kmip_norm_resident.cu, kmip_norm.cu).
+//
+// Forward: mean and variance over (nodes of a graph) x (channels of a group),
+// then y = act((x - mean) rstd w + b).  Backward: with dz = dy act'(z),
+//   db_c = sum dz,  dw_c = sum dz xhat          per channel,
+//   m1 = sum_c w_c db_c / M,  m2 = sum_c w_c dw_c / M   per graph and group,
+//   dx = rstd (dz w - m1 - xhat m2),
+// so the backward's group sums come out of the channel sums of the graph and
+// need no pass of their own.
+//
+// Bound: memory traffic.  Every pass over the rows is the same shape: a block
+// owns a slab of whole groups and a range of rows, thread (ty, tx) the V
+// channels of vector tx in every TY-th row, kRows rows in flight while the
+// next kRows are being loaded.
+//
+// Two ways over the graphs, chosen by size in plan():
+//   resident  one block per (graph, slab), one launch, for inputs that fit in
+//             L2 and where launches are what costs.  A graph of up to HOLD TY
+//             rows (512 or 1,024) stays in the threads' registers: sum, then
+//             squared deviations from the mean, then the result, with one read
+//             of x.  Longer ones are read again.
+//   split     rows of each graph cut into slots of R rows; one launch writes
+//             each slot's sums, one joins them, one walks the slots again in
+//             reverse order, so that what the first pass left in L2 is met
+//             first.  Any graph size spreads over all SMs.
+//
+// Statistics that are not held: a thread takes kRows x V values at a time,
+// forms their own mean and squared deviations (two passes over registers) and
+// joins them to its running (n, mean, M2); no difference of large sums is
+// formed in fp32.  Threads, and blocks, join in fp64 sums of n mean and
+// M2 + n mean^2.  All sums run in a fixed order: no atomics, the same bits
+// every run.
+#pragma once
+
+#include "kmip_act.cuh"
+#include "kmip_internal.h"
+
+namespace kmip {
+
+constexpr int kMaxSlabGroups = 64;
+
+struct NormParams {
+  const void *x, *w, *b, *dy;
+  void *y, *dx;
+  const int32_t* offsets;
+  float *mean, *rstd;            // [G, groups]
+  int N, C, G, groups, cg;
+  int gps;                       // groups per slab
+  float eps;
+  int R;                         // split: rows per slot
+  int slots;                     // split: N / R + G
+  double2* part;                 // split forward: [slots][groups] sums
+  float* chan;                   // backward: [blocks or slots][2][C] (db, dw)
+  const float* gchan;            // split backward: [G][2][C], per graph
+  int once;                      // larger than L2: nothing that is written or
+                                 // read for the last time should stay there
+  int* status;
+};
+
+// ------------------------------------------------------------ element access
+template <int BYTES>
+struct Raw;
+template <> struct Raw<16> { using type = uint4; };
+template <> struct Raw<4> { using type = uint32_t; };
+template <> struct Raw<2> { using type = uint16_t; };
+
+// V consecutive elements, widened to fp32.
+template <typename T, int V>
+struct Row {
+  using R = typename Raw<sizeof(T) * V>::type;
+  R raw;
+  __device__ void load(const T* p) { raw = *reinterpret_cast<const R*>(p); }
+  __device__ void load_last(const T* p) { raw = __ldcs(reinterpret_cast<const R*>(p)); }
+  __device__ void get(float (&f)[V]) const {
+    if constexpr (sizeof(T) == 4) {
+      const float* q = reinterpret_cast<const float*>(&raw);
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e] = q[e];
+    } else if constexpr (V == 1) {
+      f[0] = __uint_as_float((uint32_t)raw << 16);
+    } else {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(&raw);
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        f[2 * e] = __uint_as_float(q[e] << 16);
+        f[2 * e + 1] = __uint_as_float(q[e] & 0xffff0000u);
+      }
+    }
+  }
+  __device__ void set(const float (&f)[V]) {
+    if constexpr (sizeof(T) == 4) {
+      float* q = reinterpret_cast<float*>(&raw);
+#pragma unroll
+      for (int e = 0; e < V; ++e) q[e] = f[e];
+    } else if constexpr (V == 1) {
+      raw = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+    } else {
+      __nv_bfloat162* q = reinterpret_cast<__nv_bfloat162*>(&raw);
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) q[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+    }
+  }
+  __device__ void store(T* p, int once) const {
+    if (once) __stcs(reinterpret_cast<R*>(p), raw);
+    else *reinterpret_cast<R*>(p) = raw;
+  }
+};
+
+// ---------------------------------------------------------------- row ranges
+// Node range of graph g; false (and a status) when its offsets are malformed.
+__device__ __forceinline__ bool graph_rows(const NormParams& p, int g, int& lo, int& hi) {
+  lo = p.offsets ? p.offsets[g] : 0;
+  hi = p.offsets ? p.offsets[g + 1] : p.N;
+  const bool ok = lo >= 0 && lo <= hi && hi <= p.N && (g > 0 || lo == 0) &&
+                  (g < p.G - 1 || hi == p.N);
+  if (!ok && threadIdx.x == 0) record_status(p.status, KMIP_ERR_BAD_OFFSETS);
+  return ok;
+}
+
+// Slots: graph g owns slots [lo / R + g, ...), one per R rows; no two graphs'
+// slots meet because floor((lo + n) / R) + 1 >= floor(lo / R) + ceil(n / R).
+__device__ __forceinline__ int first_slot(const NormParams& p, int g) {
+  return (p.offsets ? p.offsets[g] : 0) / p.R + g;
+}
+
+// Graph and rows of a slot; false when the slot holds none.
+__device__ __forceinline__ bool slot_rows(const NormParams& p, int slot, int& g, int& r0,
+                                          int& r1) {
+  int a = 0, b = p.G - 1;  // last graph whose first slot is <= slot
+  while (a < b) {
+    const int m = (a + b + 1) >> 1;
+    if (first_slot(p, m) <= slot) a = m; else b = m - 1;
+  }
+  g = a;
+  int lo, hi;
+  if (!graph_rows(p, g, lo, hi)) return false;
+  const int64_t at = lo + (int64_t)(slot - first_slot(p, g)) * p.R;
+  if (at < lo || at >= hi) return false;
+  r0 = (int)at;
+  r1 = (int)min(at + p.R, (int64_t)hi);
+  return true;
+}
+
+// ------------------------------------------------------------- block's slab
+// The slab's vectors go in tiles of at most NT threads; W = tile width, TY
+// rows side by side.
+struct Slab {
+  int c0, vecs, W, TY, tx, ty, ngroups, g0;
+};
+
+template <int NT, int V>
+__device__ __forceinline__ Slab make_slab(const NormParams& p, int slab) {
+  Slab s;
+  s.g0 = slab * p.gps;
+  s.ngroups = min(p.gps, p.groups - s.g0);
+  s.c0 = s.g0 * p.cg;
+  s.vecs = s.ngroups * p.cg / V;
+  s.W = min(s.vecs, NT);
+  s.TY = NT / s.W;
+  s.tx = threadIdx.x % s.W;
+  s.ty = threadIdx.x / s.W;
+  return s;
+}
+
+// Batches of the split kernels' passes over x, and over x and dy.
+template <int V>
+constexpr int kRowsOne = V >= 4 ? 4 : 8;
+template <int V>
+constexpr int kRowsTwo = V >= 4 ? 2 : 4;
+
+// Rows r0 + ty, + TY, ... of a column in batches of KR: body(rows, r, n) with
+// the n <= KR rows r, r + TY, ..., the next batch already on its way.
+template <int KR, typename T, int V, int NIN, typename F>
+__device__ __forceinline__ void walk_rows(const Slab& s, int r0, int r1, int64_t ld,
+                                          const T* const (&col)[NIN], bool last, F&& body) {
+  const int step = KR * s.TY;
+  Row<T, V> cur[NIN][KR], nxt[NIN][KR];
+  auto fetch = [&](Row<T, V> (&dst)[NIN][KR], int r) {
+#pragma unroll
+    for (int u = 0; u < KR; ++u)
+      if (r + u * s.TY < r1) {
+#pragma unroll
+        for (int i = 0; i < NIN; ++i) {
+          const T* q = col[i] + (int64_t)(r + u * s.TY) * ld;
+          if (last) dst[i][u].load_last(q);
+          else dst[i][u].load(q);
+        }
+      }
+  };
+  int r = r0 + s.ty;
+  fetch(cur, r);
+  while (r < r1) {
+    const int rn = r + step;
+    if (rn < r1) fetch(nxt, rn);
+    body(cur, r);
+    r = rn;
+#pragma unroll
+    for (int i = 0; i < NIN; ++i)
+#pragma unroll
+      for (int u = 0; u < KR; ++u) cur[i][u] = nxt[i][u];
+  }
+}
+
+template <int NT>
+struct StatSmem {
+  double s0[NT], q[NT];
+  double gs0[kMaxSlabGroups], gq[kMaxSlabGroups];
+  float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
+};
+
+// Adds sum(n mean) and sum(M2 + n mean^2) of rows [r0, r1) to sm.gs0, sm.gq.
+template <typename T, int V, int NT, int KR>
+__device__ void slab_stats(const NormParams& p, const Slab& s, int r0, int r1,
+                           StatSmem<NT>& sm) {
+  if (threadIdx.x < s.ngroups) sm.gs0[threadIdx.x] = sm.gq[threadIdx.x] = 0.0;
+  for (int vt = 0; vt < s.vecs; vt += s.W) {
+    const int v = vt + s.tx;
+    float n = 0.f, mean = 0.f, m2 = 0.f;
+    if (s.ty < s.TY && v < s.vecs) {
+      const T* const cols[1] = {static_cast<const T*>(p.x) + s.c0 + v * V};
+      walk_rows<KR, T, V, 1>(s, r0, r1, p.C, cols, false, [&](Row<T, V> (&rows)[1][KR], int r) {
+        const int cnt = min((r1 - r + s.TY - 1) / s.TY, KR);
+        float sum = 0.f, dev = 0.f;
+#pragma unroll
+        for (int u = 0; u < KR; ++u)
+          if (u < cnt) {
+            float f[V];
+            rows[0][u].get(f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum += f[e];
+          }
+        const float nb = (float)(cnt * V);
+        const float mb = __fdividef(sum, nb);
+#pragma unroll
+        for (int u = 0; u < KR; ++u)
+          if (u < cnt) {
+            float f[V];
+            rows[0][u].get(f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const float t = f[e] - mb;
+              dev = fmaf(t, t, dev);
+            }
+          }
+        // (mb is the mean up to rounding, which the join takes as it is)
+        const float all = n + nb, d = mb - mean, share = __fdividef(nb, all);
+        mean = fmaf(d, share, mean);
+        m2 += fmaf(d * d, n * share, dev);
+        n = all;
+      });
+    }
+    sm.s0[threadIdx.x] = (double)n * mean;
+    sm.q[threadIdx.x] = (double)m2 + (double)n * mean * mean;
+    __syncthreads();
+    // one warp per group of this tile
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int vpg = p.cg / V, tile = min(s.W, s.vecs - vt);
+    for (int j = vt / vpg + warp; j < s.ngroups && j * vpg < vt + tile; j += NT / 32) {
+      const int a = max(j * vpg - vt, 0), b = min((j + 1) * vpg - vt, tile);
+      const int w = b - a;
+      double s0 = 0.0, q = 0.0;
+      for (int i = lane; i < w * s.TY; i += 32) {
+        const int at = (i / w) * s.W + a + i % w;
+        s0 += sm.s0[at];
+        q += sm.q[at];
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+        q += __shfl_xor_sync(0xffffffffu, q, o);
+      }
+      if (lane == 0) {
+        sm.gs0[j] += s0;
+        sm.gq[j] += q;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+__device__ __forceinline__ void finish_stats(double s0, double q, double count, float eps,
+                                             float& mean, float& rstd) {
+  const double m = count > 0 ? s0 / count : 0.0;
+  double var = count > 0 ? q / count - m * m : 0.0;
+  var = var < 0.0 ? 0.0 : var;  // a NaN stays
+  mean = (float)m;
+  rstd = (float)rsqrt(var + (double)eps);
+}
+
+// Channel parameters of a vector, as they are stored.
+template <typename T, int V>
+struct Affine {
+  Row<T, V> w, b;
+  __device__ void load(const NormParams& p, int c) {
+    if (p.w) {
+      w.load(static_cast<const T*>(p.w) + c);
+      b.load(static_cast<const T*>(p.b) + c);
+    } else {
+      float one[V], zero[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        one[e] = 1.f;
+        zero[e] = 0.f;
+      }
+      w.set(one);
+      b.set(zero);
+    }
+  }
+};
+
+// xhat of one element.  bf16 inputs carry 2^-9 of x already, so one fused
+// multiply-add (2^-24 of x rstd) will do; fp32 takes the difference first.
+template <typename T>
+__device__ __forceinline__ float normed(float x, float m, float rs) {
+  return sizeof(T) == 2 ? fmaf(x, rs, -m * rs) : (x - m) * rs;
+}
+
+// y of one vector.
+template <typename T, int V, int ACT>
+__device__ __forceinline__ void row_fwd(Row<T, V>& row, float m, float rs,
+                                        const Affine<T, V>& af) {
+  float f[V], w[V], b[V];
+  row.get(f);
+  af.w.get(w);
+  af.b.get(b);
+#pragma unroll
+  for (int e = 0; e < V; ++e) f[e] = act_value<T, ACT>(fmaf(normed<T>(f[e], m, rs), w[e], b[e]));
+  row.set(f);
+}
+
+// xhat, dz and the weights of one vector.
+template <typename T, int V, int ACT>
+__device__ __forceinline__ void row_bwd(const Row<T, V>& row, const Row<T, V>& grad, float m,
+                                        float rs, const Affine<T, V>& af, float (&xh)[V],
+                                        float (&dz)[V], float (&w)[V]) {
+  float b[V];
+  row.get(xh);
+  grad.get(dz);
+  af.w.get(w);
+  af.b.get(b);
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    float fa, ga;
+    xh[e] = normed<T>(xh[e], m, rs);
+    act_both<T, ACT>(fmaf(xh[e], w[e], b[e]), fa, ga);
+    dz[e] *= ga;
+  }
+}
+
+template <typename T, int V, int ACT, int KR>
+__device__ void slab_apply(const NormParams& p, const Slab& s, int r0, int r1, const float* mean,
+                           const float* rstd) {
+  if (s.ty >= s.TY) return;
+  for (int v = s.tx; v < s.vecs; v += s.W) {
+    const int c = s.c0 + v * V, j = v * V / p.cg;
+    Affine<T, V> af;
+    af.load(p, c);
+    const float m = mean[j], rs = rstd[j];
+    const T* const cols[1] = {static_cast<const T*>(p.x) + c};
+    T* out = static_cast<T*>(p.y) + c;
+    walk_rows<KR, T, V, 1>(s, r0, r1, p.C, cols, p.once, [&](Row<T, V> (&rows)[1][KR], int r) {
+#pragma unroll
+      for (int u = 0; u < KR; ++u)
+        if (r + u * s.TY < r1) {
+          row_fwd<T, V, ACT>(rows[0][u], m, rs, af);
+          rows[0][u].store(out + (int64_t)(r + u * s.TY) * p.C, p.once);
+        }
+    });
+  }
+}
+
+// ---------------------------------------------------------------- backward
+// (Dynamic shared memory: at most 42 KB.)
+template <int NT, int V>
+struct BwdSmem {
+  float red[2][NT * V / 2 * 3];  // [channel of the tile][TY, or TY + 1 if even]
+  float2 sums[NT * V];           // of the tile's channels, times weight
+  double gm1[kMaxSlabGroups], gm2[kMaxSlabGroups];
+  float m1[kMaxSlabGroups], m2[kMaxSlabGroups];
+};
+
+// Channel sums of the threads of a tile of vectors (at vector vt of the
+// slab): sdb, sdw of each thread, over ty, to dst[0][c], dst[1][c] (added to
+// what is there unless `first`); with GROUPS also added to sm.gm1, sm.gm2.
+template <typename T, int V, int NT, bool GROUPS>
+__device__ void join_channels(const NormParams& p, const Slab& s, int vt, const float (&sdb)[V],
+                              const float (&sdw)[V], float* dst, bool first, BwdSmem<NT, V>& sm) {
+  const int pitch = s.TY | 1, tile = min(s.W, s.vecs - vt) * V;
+  if (s.ty < s.TY) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      sm.red[0][(s.tx * V + e) * pitch + s.ty] = sdb[e];
+      sm.red[1][(s.tx * V + e) * pitch + s.ty] = sdw[e];
+    }
+  }
+  __syncthreads();
+  // L lanes share the threads' sums of one channel
+  int L = 1;
+  while (L < 32 && L < s.TY && tile * L * 2 <= NT) L *= 2;
+  const int part = threadIdx.x & (L - 1);
+  for (int c0 = 0; c0 < tile; c0 += NT / L) {  // uniform, for the shuffles
+    const int c = c0 + threadIdx.x / L;
+    float a = 0.f, q = 0.f;
+    if (c < tile)
+      for (int y = part; y < s.TY; y += L) {
+        a += sm.red[0][c * pitch + y];
+        q += sm.red[1][c * pitch + y];
+      }
+    for (int o = L >> 1; o; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      q += __shfl_xor_sync(0xffffffffu, q, o);
+    }
+    if (c < tile && part == 0) {
+      const int ch = s.c0 + vt * V + c;
+      dst[ch] = first ? a : dst[ch] + a;
+      dst[p.C + ch] = first ? q : dst[p.C + ch] + q;
+      if (GROUPS) {
+        const float w = p.w ? (float)static_cast<const T*>(p.w)[ch] : 1.f;
+        sm.sums[c] = make_float2(a * w, q * w);
+      }
+    }
+  }
+  __syncthreads();
+  if (GROUPS) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int base = vt * V;
+    for (int j = base / p.cg + warp; j < s.ngroups && j * p.cg < base + tile; j += NT / 32) {
+      const int a = max(j * p.cg - base, 0), b = min((j + 1) * p.cg - base, tile);
+      double s1 = 0.0, s2 = 0.0;
+      for (int i = a + lane; i < b; i += 32) {
+        s1 += sm.sums[i].x;
+        s2 += sm.sums[i].y;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+        s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+      }
+      if (lane == 0) {
+        sm.gm1[j] += s1;
+        sm.gm2[j] += s2;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Channel sums (db, dw) of rows [r0, r1), as in join_channels.
+template <typename T, int V, int ACT, int NT, bool GROUPS, int KR>
+__device__ void slab_bwd_sums(const NormParams& p, const Slab& s, int r0, int r1,
+                              const float* mean, const float* rstd, float* dst, bool first,
+                              BwdSmem<NT, V>& sm) {
+  for (int vt = 0; vt < s.vecs; vt += s.W) {
+    const int v = vt + s.tx;
+    float sdb[V], sdw[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) sdb[e] = sdw[e] = 0.f;
+    if (s.ty < s.TY && v < s.vecs) {
+      const int c = s.c0 + v * V, j = v * V / p.cg;
+      Affine<T, V> af;
+      af.load(p, c);
+      const float m = mean[j], rs = rstd[j];
+      const T* const cols[2] = {static_cast<const T*>(p.x) + c, static_cast<const T*>(p.dy) + c};
+      walk_rows<KR, T, V, 2>(s, r0, r1, p.C, cols, false, [&](Row<T, V> (&rows)[2][KR], int r) {
+#pragma unroll
+        for (int u = 0; u < KR; ++u)
+          if (r + u * s.TY < r1) {
+            float xh[V], dz[V], w[V];
+            row_bwd<T, V, ACT>(rows[0][u], rows[1][u], m, rs, af, xh, dz, w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              sdb[e] += dz[e];
+              sdw[e] = fmaf(dz[e], xh[e], sdw[e]);
+            }
+          }
+      });
+    }
+    join_channels<T, V, NT, GROUPS>(p, s, vt, sdb, sdw, dst, first, sm);
+  }
+}
+
+template <typename T, int V, int ACT, int KR>
+__device__ void slab_bwd_apply(const NormParams& p, const Slab& s, int r0, int r1,
+                               const float* mean, const float* rstd, const float* m1,
+                               const float* m2) {
+  if (s.ty >= s.TY) return;
+  for (int v = s.tx; v < s.vecs; v += s.W) {
+    const int c = s.c0 + v * V, j = v * V / p.cg;
+    Affine<T, V> af;
+    af.load(p, c);
+    const float m = mean[j], rs = rstd[j], a1 = m1[j], a2 = m2[j];
+    const T* const cols[2] = {static_cast<const T*>(p.x) + c, static_cast<const T*>(p.dy) + c};
+    T* out = static_cast<T*>(p.dx) + c;
+    walk_rows<KR, T, V, 2>(s, r0, r1, p.C, cols, p.once, [&](Row<T, V> (&rows)[2][KR], int r) {
+#pragma unroll
+      for (int u = 0; u < KR; ++u)
+        if (r + u * s.TY < r1) {
+          float xh[V], dz[V], w[V];
+          row_bwd<T, V, ACT>(rows[0][u], rows[1][u], m, rs, af, xh, dz, w);
+#pragma unroll
+          for (int e = 0; e < V; ++e) dz[e] = rs * (fmaf(dz[e], w[e], -a1) - xh[e] * a2);
+          rows[1][u].set(dz);
+          rows[1][u].store(out + (int64_t)(r + u * s.TY) * p.C, p.once);
+        }
+    });
+  }
+}
+
+// Copies the statistics of graph g's slab to shared memory.
+__device__ __forceinline__ void load_stats(const NormParams& p, const Slab& s, int g, float* mean,
+                                           float* rstd) {
+  if (threadIdx.x < s.ngroups) {
+    mean[threadIdx.x] = p.mean[(int64_t)g * p.groups + s.g0 + threadIdx.x];
+    rstd[threadIdx.x] = p.rstd[(int64_t)g * p.groups + s.g0 + threadIdx.x];
+  }
+}
+
+// The resident kernels (kmip_norm_resident.cu); p.gps is set.  norm_bwd_blocks:
+// rows of p.chan that the backward writes.
+int norm_resident_blocks(const NormParams& p, int slabs);
+cudaError_t launch_norm_fwd_resident(kmip_dtype_t dtype, int v, int act, const NormParams& p,
+                                     int slabs, cudaStream_t stream);
+cudaError_t launch_norm_bwd_resident(kmip_dtype_t dtype, int v, int act, const NormParams& p,
+                                     int slabs, cudaStream_t stream);
+
+// Calls f.template operator()<T, V, ACT>() for the element type, the vector
+// width and the activation.
+template <typename F>
+cudaError_t norm_dispatch(kmip_dtype_t dtype, int v, int act, F&& f) {
+  cudaError_t e = cudaErrorInvalidValue;
+  KMIP_ACT_SWITCH(act, {
+    if (dtype == KMIP_BF16)
+      e = v == 8   ? f.template operator()<__nv_bfloat16, 8, ACT>()
+          : v == 2 ? f.template operator()<__nv_bfloat16, 2, ACT>()
+                   : f.template operator()<__nv_bfloat16, 1, ACT>();
+    else
+      e = v == 4 ? f.template operator()<float, 4, ACT>() : f.template operator()<float, 1, ACT>();
+  })
+  return e;
+}
+
+}  // namespace kmip
