@@ -48,11 +48,17 @@ extern "C" __attribute__((visibility("default"))) kmip_status_t kmip_ffn_fwd(
   const size_t nf = (size_t)N * F;
   void* scratch = nullptr;
   cudaError_t e;
-  if (dtype == KMIP_BF16) {
-    e = scratch_alloc(&scratch, 2 * nf, stream);
+  if (N <= kFfnFewRows) {
+    e = scratch_alloc(&scratch, 4 * nf, stream);
+    if (e != cudaSuccess) return to_status(e);
+    e = launch_ffn_rows_fwd(dtype, a, static_cast<float*>(scratch), y, stream);
+  } else if (dtype == KMIP_BF16) {
+    const size_t mat = round16(2 * nf);
+    e = scratch_alloc(&scratch, mat + ffn_fwd_scratch(a), stream);
     if (e != cudaSuccess) return to_status(e);
     e = launch_ffn_glu(a, scratch, stream);
-    if (e == cudaSuccess) e = launch_ffn_down(a, scratch, y, stream);
+    if (e == cudaSuccess)
+      e = launch_ffn_down(a, scratch, y, static_cast<char*>(scratch) + mat, stream);
   } else {
     e = scratch_alloc(&scratch, 8 * nf + ffn_f32_scratch(), stream);
     if (e != cudaSuccess) return to_status(e);
@@ -86,11 +92,11 @@ extern "C" __attribute__((visibility("default"))) kmip_status_t kmip_ffn_bwd(
   void* scratch = nullptr;
   if (dtype == KMIP_BF16) {
     const size_t mat = round16(2 * nf);
-    e = scratch_alloc(&scratch, 3 * mat + ffn_wgrad_scratch(a), stream);
+    e = scratch_alloc(&scratch, 3 * mat + ffn_bwd_scratch(a), stream);
     if (e != cudaSuccess) return to_status(e);
     char *da = static_cast<char*>(scratch), *db = da + mat, *h = db + mat;
     e = launch_ffn_glu_bwd(a, dy, da, db, h, stream);
-    if (e == cudaSuccess) e = launch_ffn_dx(a, da, db, dx, stream);
+    if (e == cudaSuccess) e = launch_ffn_dx(a, da, db, dx, h + mat, stream);
     if (e == cudaSuccess)
       e = launch_ffn_wgrad(a, dy, da, db, h, dWg, dWu, dWd, h + mat, stream);
   } else {

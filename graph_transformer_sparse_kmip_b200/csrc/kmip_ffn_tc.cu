@@ -24,9 +24,12 @@
 // to TMA stores through a corner of shared memory of their own, so no warp
 // waits for another.  (Stores from registers, 32 bytes a lane, took 2.3
 // cycles a sector: 7,700 cycles for dA, dB, h of a 256 x 128 tile.)
-// Accumulators are double-buffered; the backward's three need 384 of 512
+// Accumulators are double-buffered.  The backward's three need 384 of 512
 // columns, so there dh alone has two buffers, and dh of the next tile runs
-// while a and b are read.
+// while a and b are read.  (A step of 128 columns takes a pair as long as one
+// of 256, 541 cycles, so dh costs twice its share.  As a product of its own
+// with 256 columns, through 4 N F bytes of memory, it was no faster: 1.55 for
+// 1.51 ms of a training step at 31,623 x 1,024 x 2,816.)
 //
 // The weight gradients contract over N: both operands have the contraction
 // index outermost.  Tiles that fill all clusters are computed whole, all
@@ -83,12 +86,12 @@ struct GemmParams {
   int rows, cols;      // output extent (kGlu, kGluBwd: N x F)
   int tiles_n;         // column tiles
   int tiles;           // all tiles
-  int kb0, kb1;        // steps of the two segments
+  int kb0, kb1;        // steps of the contraction, or of its two segments
+  int whole;           // tiles computed whole
+  int parts;           // parts of each of the others
+  float4* part;        // their partial tiles, joined into out[0] (kNT, kNN) or
+  __nv_bfloat16* out[3];  // dWg, dWu [rows][cols], dWd [cols][rows] (kTN)
   int tiles_p;         // kTN: row tiles of one of the three gradients
-  int whole;           // kTN: tiles computed whole
-  int parts;           // kTN: parts of each of the others
-  float4* part;        // kTN: their partial tiles
-  __nv_bfloat16 *dwg, *dwu, *dwd;  // kTN: [rows][cols] twice, [cols][rows]
   int* status;
 };
 
@@ -98,28 +101,26 @@ struct Item {
   int tile, k0, kn, slot;
 };
 
-// Cluster c takes tiles c, c + clusters, ...; kTN: first whole tiles like
-// that, then parts, numbered with the tile running fastest, likewise.
-template <int MODE>
+// Cluster c takes tiles c, c + clusters, ...: first whole ones, then parts of
+// the others, numbered with the tile running fastest.
 struct Walk {
   int64_t i;
-  int clusters;
-  __device__ Walk(int c, int n) : i(c), clusters(n) {}
+  int clusters, steps;
+  __device__ Walk(int c, int n, int steps_) : i(c), clusters(n), steps(steps_) {}
   __device__ bool next(const GemmParams& p, Item& it) {
-    if (MODE == kTN && i >= p.whole) {
+    if (i >= p.whole) {
       const int rest = p.tiles - p.whole;
       const int64_t j = i - p.whole;
       if (j >= (int64_t)rest * p.parts) return false;
       const int s = (int)(j / rest);
       it.tile = p.whole + (int)(j % rest);
-      it.k0 = (int)((int64_t)p.kb0 * s / p.parts);
-      it.kn = (int)((int64_t)p.kb0 * (s + 1) / p.parts) - it.k0;
+      it.k0 = (int)((int64_t)steps * s / p.parts);
+      it.kn = (int)((int64_t)steps * (s + 1) / p.parts) - it.k0;
       it.slot = p.parts > 1 ? (int)j : -1;
     } else {
-      if (i >= p.tiles) return false;
       it.tile = (int)i;
       it.k0 = 0;
-      it.kn = p.kb0;
+      it.kn = steps;
       it.slot = -1;
     }
     i += clusters;
@@ -152,7 +153,9 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
   constexpr int kBufs = MODE == kGluBwd ? 1 : 2;
   constexpr int kBufCols = MODE == kGluBwd ? 0 : BN;
   constexpr int kTmemCols = MODE == kGluBwd ? 512 : 2 * BN;
-  constexpr int kSegs = MODE == kNN || MODE == kGluBwd ? 2 : 1;
+  constexpr int kSegs = MODE == kGluBwd ? 2 : 1;
+  // kNN's two products are one contraction here
+  const int steps = MODE == kNN ? p.kb0 + p.kb1 : p.kb0;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -196,13 +199,13 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
     if (lane == 0) {
       const uint32_t full0 = map_to_cta(full, 0);
       uint32_t it_no = 0;
-      Walk<MODE> walk(cluster, clusters);
+      Walk walk(cluster, clusters, steps);
       Item it;
       bool ok = true;
       while (ok && walk.next(p, it)) {
         const int mt = it.tile / p.tiles_n, nt = it.tile % p.tiles_n;
         for (int seg = 0; seg < kSegs && ok; ++seg) {
-          const int kn = seg ? p.kb1 : (MODE == kTN ? it.kn : p.kb0);
+          const int kn = seg ? p.kb1 : it.kn;
           for (int kb = 0; kb < kn; ++kb, ++it_no) {
             const uint32_t s = it_no % kStages, ph = (it_no / kStages) & 1;
             if (!mbar_wait(empty + 8 * s, ph ^ 1, abort_flag, kTimeoutNs)) {
@@ -223,11 +226,13 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
               tma_load_2d_pair(a, &maps.m[0], bar, k, mt * kTileM + rank * kHalfM);
               tma_load_2d_pair(b, &maps.m[1], bar, k, nt * BN + rank * (BN / 2));
             } else if constexpr (MODE == kNN) {
-              tma_load_2d_pair(a, &maps.m[seg], bar, k, mt * kTileM + rank * kHalfM);
+              const int second = it.k0 + kb >= p.kb0;
+              const int ks = k - second * p.kb0 * kBK;
+              tma_load_2d_pair(a, &maps.m[second], bar, ks, mt * kTileM + rank * kHalfM);
 #pragma unroll
               for (int j = 0; j < BN / 128; ++j)
-                tma_load_2d_pair(b + j * 8192, &maps.m[2 + seg], bar,
-                                 nt * BN + rank * (BN / 2) + 64 * j, k);
+                tma_load_2d_pair(b + j * 8192, &maps.m[2 + second], bar,
+                                 nt * BN + rank * (BN / 2) + 64 * j, ks);
             } else if constexpr (MODE == kGluBwd) {
               if (seg == 0) {
                 tma_load_2d_pair(a, &maps.m[0], bar, k, mt * kTileM + rank * kHalfM);
@@ -253,7 +258,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
     // ----------------------------------------------------------------- MMA
     if (lane == 0 && rank == 0) {
       uint32_t it_no = 0, tile_no = 0;
-      Walk<MODE> walk(cluster, clusters);
+      Walk walk(cluster, clusters, steps);
       Item it;
       bool ok = true;
       while (ok && walk.next(p, it)) {
@@ -284,8 +289,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
                                                                         : BN;
           const uint32_t idesc = idesc_bf16_f32(kTileM, n) | (a_outer ? kIdescAOuterK : 0u) |
                                  (b_outer ? kIdescBOuterK : 0u);
-          const int kn = seg ? p.kb1 : (MODE == kTN ? it.kn : p.kb0);
-          const bool keep = MODE == kNN && seg == 1;  // adds to the first segment
+          const int kn = seg ? p.kb1 : it.kn;
           for (int kb = 0; kb < kn; ++kb, ++it_no) {
             const uint32_t s = it_no % kStages, ph = (it_no / kStages) & 1;
             if (!mbar_wait_cluster(full + 8 * s, ph, abort_flag, kTimeoutNs)) {
@@ -300,7 +304,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
             const uint64_t sa = a_outer ? 128 : 2, sb = b_outer ? 128 : 2;
 #pragma unroll
             for (int q = 0; q < kBK / 16; ++q)
-              mma_bf16_pair(d, da + q * sa, db + q * sb, idesc, kb || q || keep);
+              mma_bf16_pair(d, da + q * sa, db + q * sb, idesc, kb || q);
             mma_commit_pair(empty + 8 * s);
           }
         }
@@ -328,7 +332,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
       }
     };
     uint32_t tile_no = 0;
-    Walk<MODE> walk(cluster, clusters);
+    Walk walk(cluster, clusters, steps);
     Item it;
     while (walk.next(p, it)) {
       const int mt = it.tile / p.tiles_n, nt = it.tile % p.tiles_n;
@@ -408,8 +412,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
         send(3, 0, f0, m0);
       } else {
         const int prob = MODE == kTN ? mt / p.tiles_p : 0;
-        float4* part =
-            MODE == kTN ? p.part + ((int64_t)it.slot * 2 + rank) * (BN / 4 * kHalfM) : nullptr;
+        float4* part = p.part + ((int64_t)it.slot * 2 + rank) * (BN / 4 * kHalfM);
 #pragma unroll 1
         for (int j = 0; j < BN / 128; ++j) {
           const int col = quarter * (BN / 4) + j * 32, n = nt * BN + col;
@@ -418,7 +421,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
           tmem_ld_wait_all();
           reg_fence(v);
           if (j == BN / 128 - 1) release();
-          if (MODE == kTN && it.slot >= 0) {
+          if (it.slot >= 0) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               part[(int64_t)(col / 4 + e) * kHalfM + row] =
@@ -429,7 +432,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (n + e < p.cols)
-                  p.dwd[(int64_t)(n + e) * p.rows + m0 + lane] = __float2bfloat16_rn(v[e]);
+                  p.out[2][(int64_t)(n + e) * p.rows + m0 + lane] = __float2bfloat16_rn(v[e]);
             }
           } else {
             uint32_t w[2][8];
@@ -460,7 +463,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
   }
 }
 
-// Adds the partial tiles of the weight gradients in order.  Grid: (tile that
+// Adds partial tiles in order.  Grid: (tile that
 // was cut, CTA of the pair, 8-column group); 128 threads, one per row.
 template <int BN>
 __global__ void __launch_bounds__(128) ffn_join_kernel(const GemmParams p) {
@@ -489,9 +492,9 @@ __global__ void __launch_bounds__(128) ffn_join_kernel(const GemmParams p) {
     const float f[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      p.dwd[(int64_t)(c + e) * p.rows + r] = __float2bfloat16_rn(f[e]);
+      p.out[2][(int64_t)(c + e) * p.rows + r] = __float2bfloat16_rn(f[e]);
   } else {
-    *reinterpret_cast<uint4*>((prob ? p.dwu : p.dwg) + (int64_t)r * p.cols + c) =
+    *reinterpret_cast<uint4*>((prob ? p.out[1] : p.out[0]) + (int64_t)r * p.cols + c) =
         make_uint4(pack2(v[0].x, v[0].y), pack2(v[0].z, v[0].w), pack2(v[1].x, v[1].y),
                    pack2(v[1].z, v[1].w));
   }
@@ -533,16 +536,73 @@ int tile_cols(int cols) {
   return ceil_div(cols, 256) * 256 * 4 >= ceil_div(cols, 128) * 128 * 5 ? 128 : 256;
 }
 
-// Output of rows x cols in tiles of kTileM x bn, a contraction of length k.
-GemmParams params(const FfnArgs& a, int rows, int cols, int bn, int k) {
+// Steps of the contraction that a part costs beside its products (its first
+// loads, its partial tile written and read again by one more launch: 5 to 6 us
+// where a step takes 0.4 us).
+constexpr int kPartCost = 14;
+
+// Output of rows x cols in tiles of kTileM x bn, a contraction of length k;
+// `times` outputs side by side (kTN), `segs` contractions after one another.
+// With `split`, tiles beyond what fills all clusters evenly are cut into the
+// number of parts whose last round of clusters idles least.
+GemmParams params(const FfnArgs& a, int rows, int cols, int bn, int k, bool split = false,
+                  int segs = 1, int times = 1) {
   GemmParams p{};
   p.rows = rows;
   p.cols = cols;
   p.tiles_n = ceil_div(cols, bn);
-  p.tiles = ceil_div(rows, kTileM) * p.tiles_n;
+  p.tiles_p = ceil_div(rows, kTileM);
+  p.tiles = times * p.tiles_p * p.tiles_n;
   p.kb0 = p.kb1 = ceil_div(k, kBK);
+  p.whole = p.tiles;
+  p.parts = 1;
   p.status = a.status;
+  if (split) {
+    const int all = device_sm_count() / 2, steps = segs * p.kb0;
+    p.whole = p.tiles / all * all;
+    const int rest = p.tiles - p.whole;
+    int64_t best = rest ? steps - kPartCost : 0;  // or left whole
+    for (int s = 2; s <= steps && (int64_t)rest * s <= 4 * all; ++s) {
+      const int64_t cost =
+          (int64_t)ceil_div((int64_t)rest * s, all) * (ceil_div(steps, s) + kPartCost);
+      if (cost < best) {
+        best = cost;
+        p.parts = s;
+      }
+    }
+    if (p.parts == 1) p.whole = p.tiles;
+  }
   return p;
+}
+
+size_t part_bytes(const GemmParams& p, int bn) {
+  return (size_t)(p.tiles - p.whole) * p.parts * kTileM * bn * sizeof(float);
+}
+
+// The GEMM and, where tiles were cut, the join of their parts.
+template <int MODE>
+cudaError_t launch_split(const Maps& m, const GemmParams& p, int bn, cudaStream_t stream) {
+  const int rest = p.tiles - p.whole;
+  const int c = clusters_for(p.whole + (int64_t)rest * p.parts);
+  const cudaError_t e = bn == 256 ? launch_gemm<MODE, 256, 0>(m, p, c, stream)
+                                  : launch_gemm<MODE, 128, 0>(m, p, c, stream);
+  if (e != cudaSuccess || !rest) return e;
+  const dim3 grid(rest, 2, bn / 8);
+  if (bn == 256)
+    ffn_join_kernel<256><<<grid, 128, 0, stream>>>(p);
+  else
+    ffn_join_kernel<128><<<grid, 128, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+GemmParams down_params(const FfnArgs& a, int bn) {
+  return params(a, a.N, a.C, bn, a.F, true);
+}
+GemmParams dx_params(const FfnArgs& a, int bn) {
+  return params(a, a.N, a.C, bn, a.F, true, 2);
+}
+GemmParams wgrad_params(const FfnArgs& a, int bn) {
+  return params(a, a.F, a.C, bn, a.N, true, 1, 3);
 }
 
 bool out_map(CUtensorMap* m, const void* ptr, int rows, int cols) {
@@ -561,16 +621,22 @@ cudaError_t launch_ffn_glu(const FfnArgs& a, void* h, cudaStream_t stream) {
   return launch_act<kGlu>(a.act, m, p, stream);
 }
 
-cudaError_t launch_ffn_down(const FfnArgs& a, const void* h, void* y, cudaStream_t stream) {
+size_t ffn_fwd_scratch(const FfnArgs& a) {
+  const int bn = tile_cols(a.C);
+  return part_bytes(down_params(a, bn), bn);
+}
+
+cudaError_t launch_ffn_down(const FfnArgs& a, const void* h, void* y, void* scratch,
+                            cudaStream_t stream) {
   Maps m;
   const int bn = tile_cols(a.C);
-  const GemmParams p = params(a, a.N, a.C, bn, a.F);
+  GemmParams p = down_params(a, bn);
+  p.part = static_cast<float4*>(scratch);
+  p.out[0] = static_cast<__nv_bfloat16*>(y);
   if (!encode_map_2d(&m.m[0], h, a.N, a.F, 64, kHalfM) ||
       !encode_map_2d(&m.m[1], a.wd, a.C, a.F, 64, bn / 2) || !out_map(&m.out[0], y, a.N, a.C))
     return cudaErrorInvalidValue;
-  const int c = clusters_for(p.tiles);
-  return bn == 256 ? launch_gemm<kNT, 256, 0>(m, p, c, stream)
-                   : launch_gemm<kNT, 128, 0>(m, p, c, stream);
+  return launch_split<kNT>(m, p, bn, stream);
 }
 
 cudaError_t launch_ffn_glu_bwd(const FfnArgs& a, const void* dy, void* da, void* db, void* h,
@@ -587,60 +653,25 @@ cudaError_t launch_ffn_glu_bwd(const FfnArgs& a, const void* dy, void* da, void*
   return launch_act<kGluBwd>(a.act, m, p, stream);
 }
 
+size_t ffn_bwd_scratch(const FfnArgs& a) {
+  const int bn = tile_cols(a.C);
+  const size_t x = part_bytes(dx_params(a, bn), bn), w = part_bytes(wgrad_params(a, bn), bn);
+  return x > w ? x : w;
+}
+
 cudaError_t launch_ffn_dx(const FfnArgs& a, const void* da, const void* db, void* dx,
-                          cudaStream_t stream) {
+                          void* scratch, cudaStream_t stream) {
   Maps m;
   const int bn = tile_cols(a.C);
-  const GemmParams p = params(a, a.N, a.C, bn, a.F);
+  GemmParams p = dx_params(a, bn);
+  p.part = static_cast<float4*>(scratch);
+  p.out[0] = static_cast<__nv_bfloat16*>(dx);
   if (!encode_map_2d(&m.m[0], da, a.N, a.F, 64, kHalfM) ||
       !encode_map_2d(&m.m[1], db, a.N, a.F, 64, kHalfM) ||
       !encode_map_2d(&m.m[2], a.wg, a.F, a.C, 64, kBK) ||
       !encode_map_2d(&m.m[3], a.wu, a.F, a.C, 64, kBK) || !out_map(&m.out[0], dx, a.N, a.C))
     return cudaErrorInvalidValue;
-  const int c = clusters_for(p.tiles);
-  return bn == 256 ? launch_gemm<kNN, 256, 0>(m, p, c, stream)
-                   : launch_gemm<kNN, 128, 0>(m, p, c, stream);
-}
-
-namespace {
-
-// Steps of 64 rows that a part costs beside its products (its first loads,
-// its partial tile written and read again).
-constexpr int kPartCost = 8;
-
-// Whole tiles and parts of the weight gradients.
-GemmParams wgrad_params(const FfnArgs& a, int bn, void* dwg, void* dwu, void* dwd) {
-  GemmParams p = params(a, a.F, a.C, bn, a.N);
-  p.dwg = static_cast<__nv_bfloat16*>(dwg);
-  p.dwu = static_cast<__nv_bfloat16*>(dwu);
-  p.dwd = static_cast<__nv_bfloat16*>(dwd);
-  p.tiles_p = ceil_div(a.F, kTileM);
-  p.tiles *= 3;
-  const int all = device_sm_count() / 2;
-  p.whole = p.tiles / all * all;
-  const int rest = p.tiles - p.whole;
-  p.parts = 1;
-  if (rest) {
-    // the number of parts whose last round of clusters idles least
-    int64_t best = INT64_MAX;
-    for (int s = 1; s <= p.kb0 && (int64_t)rest * s <= 4 * all; ++s) {
-      const int64_t cost = (int64_t)ceil_div((int64_t)rest * s, all) *
-                           (ceil_div(p.kb0, s) + (s > 1 ? kPartCost : 0));
-      if (cost < best) {
-        best = cost;
-        p.parts = s;
-      }
-    }
-  }
-  return p;
-}
-
-}  // namespace
-
-size_t ffn_wgrad_scratch(const FfnArgs& a) {
-  const int bn = tile_cols(a.C);
-  const GemmParams p = wgrad_params(a, bn, nullptr, nullptr, nullptr);
-  return p.parts > 1 ? (size_t)(p.tiles - p.whole) * p.parts * kTileM * bn * sizeof(float) : 0;
+  return launch_split<kNN>(m, p, bn, stream);
 }
 
 cudaError_t launch_ffn_wgrad(const FfnArgs& a, const void* dy, const void* da, const void* db,
@@ -648,8 +679,11 @@ cudaError_t launch_ffn_wgrad(const FfnArgs& a, const void* dy, const void* da, c
                              cudaStream_t stream) {
   Maps m;
   const int bn = tile_cols(a.C);
-  GemmParams p = wgrad_params(a, bn, dwg, dwu, dwd);
+  GemmParams p = wgrad_params(a, bn);
   p.part = static_cast<float4*>(scratch);
+  p.out[0] = static_cast<__nv_bfloat16*>(dwg);
+  p.out[1] = static_cast<__nv_bfloat16*>(dwu);
+  p.out[2] = static_cast<__nv_bfloat16*>(dwd);
   if (!encode_map_2d(&m.m[0], da, a.N, a.F, 64, kBK) ||
       !encode_map_2d(&m.m[1], db, a.N, a.F, 64, kBK) ||
       !encode_map_2d(&m.m[2], h, a.N, a.F, 64, kBK) ||
@@ -657,17 +691,7 @@ cudaError_t launch_ffn_wgrad(const FfnArgs& a, const void* dy, const void* da, c
       !encode_map_2d(&m.m[4], dy, a.N, a.C, 64, kBK) || !out_map(&m.out[0], dwg, a.F, a.C) ||
       !out_map(&m.out[1], dwu, a.F, a.C))
     return cudaErrorInvalidValue;
-  const int rest = p.tiles - p.whole;
-  const int c = clusters_for(p.whole + (int64_t)rest * p.parts);
-  cudaError_t e = bn == 256 ? launch_gemm<kTN, 256, 0>(m, p, c, stream)
-                            : launch_gemm<kTN, 128, 0>(m, p, c, stream);
-  if (e != cudaSuccess || p.parts == 1) return e;
-  const dim3 grid(rest, 2, bn / 8);
-  if (bn == 256)
-    ffn_join_kernel<256><<<grid, 128, 0, stream>>>(p);
-  else
-    ffn_join_kernel<128><<<grid, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_split<kTN>(m, p, bn, stream);
 }
 
 }  // namespace kmip
