@@ -1,0 +1,202 @@
+"""The operators around the attention through torch autograd, alone and run
+together as a GraphTransformerLayer, against fp64 on the CPU.
+
+The layer's reference applies the same parameters in fp64 and takes the
+attention over the GPU-selected key sets from the oracle, so every gradient is
+compared through the whole layer.  The tolerance is the attention block's, 2e-2
+of the largest entry for bf16: five half steps of 2^-8, where the layer rounds
+to bf16 some eight times in a row and independent roundings add as the root of
+their number (2.9 half steps)."""
+import math
+
+import pytest
+import torch
+
+import oracle
+from graph_transformer_sparse_kmip_b200 import binding
+from graph_transformer_sparse_kmip_b200 import workloads as wl
+from graph_transformer_sparse_kmip_b200.layer import (AxisRotary, GatedFeedForward,
+                                                      GraphGroupNorm, GraphTransformerLayer,
+                                                      KmipGlobalAttention)
+from parity import check_values
+from test_gpu_layer import _OracleAttention
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    binding.load()
+    return torch.device("cuda:0")
+
+
+def _norm64(x, w, b, offsets, groups, eps):
+    out = []
+    for part in x.split(offsets.diff().tolist()):
+        p = part.unflatten(1, (groups, -1))
+        if len(p):
+            m = p.mean((0, 2), keepdim=True)
+            v = (p - m).square().mean((0, 2), keepdim=True)
+            p = (p - m) * (v + eps) ** -0.5
+        out.append(p.flatten(1))
+    return torch.cat(out) * w + b
+
+
+def _turn64(x, pos, rotary):
+    ang = pos.double()[:, rotary._axis] * torch.tensor(rotary._freq, dtype=torch.float64)
+    c, s = ang.cos()[:, None], ang.sin()[:, None]
+    P = ang.shape[1]
+    u, v = x[..., :P], x[..., P:2 * P]
+    return torch.cat([u * c - v * s, u * s + v * c, x[..., 2 * P:]], -1)
+
+
+@pytest.mark.parametrize("axes", [0, 2, 3])
+def test_layer_matches_fp64(dev, axes):
+    sizes, hidden, heads, k, width, groups = [300, 45, 0, 517, 129], 128, 4, 15, 344, 8
+    d, N = hidden // heads, sum(sizes)
+    gen = torch.Generator().manual_seed(40 + axes)
+    offsets = wl.offsets_from_sizes(sizes)
+    torch.manual_seed(3)
+    layer = GraphTransformerLayer(hidden, heads, k, width, groups, axes=axes, device=dev)
+    with torch.no_grad():
+        for norm in (layer.norm1, layer.norm2):
+            norm.weight += 0.2 * torch.randn_like(norm.weight)
+            norm.bias += 0.2 * torch.randn_like(norm.bias)
+    x = torch.randn((N, hidden), generator=gen).to(BF).to(dev).requires_grad_(True)
+    gy = torch.randn((N, hidden), generator=gen).to(BF).to(dev)
+    pos = (torch.rand((N, axes), generator=gen) * 4).to(dev) if axes else None
+    y = layer(x, offsets.to(dev), pos)
+    y.backward(gy)
+    torch.cuda.synchronize()
+    binding.check_status()
+
+    P = {n: p.detach().cpu().double().requires_grad_(True) for n, p in layer.named_parameters()}
+    x64 = x.detach().cpu().double().requires_grad_(True)
+    h = _norm64(x64, P["norm1.weight"], P["norm1.bias"], offsets, groups, 1e-5)
+    qkv = (h @ P["attn.qkv.weight"].T + P["attn.qkv.bias"]).view(N, 3, heads, d)
+    q, kk = qkv[:, 0], qkv[:, 1]
+    if axes:
+        q, kk = (_turn64(t, pos.cpu(), layer.attn.rotary) for t in (q, kk))
+    a = _OracleAttention.apply(q.contiguous(), kk.contiguous(), qkv[:, 2].contiguous(),
+                               layer.attn.last_idx.cpu().numpy(), offsets.numpy(),
+                               1.0 / math.sqrt(d))
+    z = x64 + a.reshape(N, hidden) @ P["attn.proj.weight"].T + P["attn.proj.bias"]
+    m = _norm64(z, P["norm2.weight"], P["norm2.bias"], offsets, groups, 1e-5)
+    g = torch.nn.functional.silu(m @ P["ffn.gate"].T) * (m @ P["ffn.up"].T)
+    y64 = z + g @ P["ffn.down"].T
+    y64.backward(gy.cpu().double())
+
+    check_values("y", y, y64.detach(), BF)
+    check_values("dx", x.grad, x64.grad, BF)
+    for n, p in layer.named_parameters():
+        got, ref = p.grad, P[n].grad
+        if got.dim() == 1:
+            got, ref = got[None], ref[None]
+        check_values("d" + n, got, ref, BF)
+
+
+def test_gradients_match_differences(dev):
+    """fp32 modules against central differences of the fp64-summed loss: step
+    h = 2^-6 gives a difference quotient that is off by h^2 / 6 of the third
+    derivative (under 1e-3 of the gradient's size here) and by the forward's
+    fp32 error over h (2^-22 * 64)."""
+    torch.manual_seed(1)
+    x = torch.randn(40, 32, device=dev)
+    offsets = torch.tensor([0, 25, 40], dtype=torch.int32, device=dev)
+    pos = torch.rand(40, 2, device=dev)
+    rot = AxisRotary(16, 2, interleaved=True)
+    cases = [(GraphGroupNorm(32, 4, act="silu", dtype=F32, device=dev), (offsets,)),
+             (GatedFeedForward(32, 48, dtype=F32, device=dev), ()),
+             (lambda t, p: rot(t.view(40, 2, 16), p).reshape(40, 32), (pos,))]
+    for f, extra in cases:
+        w = torch.randn(40, 32, device=dev)
+        leaf = x.clone().requires_grad_(True)
+        (f(leaf, *extra) * w).sum().backward()
+        step = 2.0 ** -6
+        for i, j in ((0, 0), (7, 31), (24, 16), (39, 5)):
+            vals = []
+            for sgn in (1, -1):
+                t = x.clone()
+                t[i, j] += sgn * step
+                vals.append((f(t, *extra).double() * w.double()).sum())
+            quotient = ((vals[0] - vals[1]) / (2 * step)).item()
+            assert abs(quotient - leaf.grad[i, j].item()) <= 5e-3 * max(
+                1.0, leaf.grad.abs().max().item())
+
+
+def test_strided_and_expanded_gradients(dev):
+    """Gradients that arrive transposed or broadcast."""
+    rot = AxisRotary(32, 2)
+    pos = torch.rand(50, 2, device=dev)
+    x = torch.randn(50, 4, 32, device=dev, requires_grad=True)
+    rot(x, pos).transpose(1, 2).sum(1).sum().backward()
+    g1 = x.grad.clone()
+    x.grad = None
+    y = rot(x, pos)
+    y.backward(torch.ones(1, 1, 1, device=dev).expand(50, 4, 32))
+    assert torch.equal(g1, x.grad)
+    ffn = GatedFeedForward(32, 64, dtype=F32, device=dev)
+    norm = GraphGroupNorm(32, 4, dtype=F32, device=dev)
+    z = torch.randn(32, 50, device=dev, requires_grad=True)
+    ffn(norm(z.t())).sum().backward()       # x itself transposed
+    assert z.grad.shape == (32, 50) and torch.isfinite(z.grad).all()
+
+
+def test_refusals(dev):
+    with pytest.raises(ValueError, match="multiple"):
+        GraphGroupNorm(30, 4)
+    with pytest.raises(ValueError, match="multiples of 8"):
+        GatedFeedForward(36, 64)
+    with pytest.raises(ValueError, match="activation"):
+        GatedFeedForward(32, 64, act="tanh")
+    with pytest.raises(ValueError, match="sections"):
+        AxisRotary(32, 2, sections=[10, 7])
+    rot = AxisRotary(32, 2)
+    with pytest.raises(ValueError, match="no gradient"):
+        rot(torch.zeros(4, 2, 32, device=dev), torch.zeros(4, 2, device=dev, requires_grad=True))
+    blk = KmipGlobalAttention(64, 2, 4, dtype=BF, device=dev, rotary=rot)
+    with pytest.raises(ValueError, match="positions"):
+        blk(torch.zeros(8, 64, dtype=BF, device=dev))
+
+
+def test_module_casts_keep_the_frequencies(dev):
+    rot = AxisRotary(32, 2)
+    m = torch.nn.Sequential(rot).to(BF).to(dev)
+    freq, axis = m[0].tables(dev)
+    assert freq.dtype == torch.float64 and axis.dtype == torch.int32
+
+
+def test_captured_training_step(dev):
+    """Forward and backward of the layer captured into a graph, replayed with
+    new inputs, against the eager gradients."""
+    torch.manual_seed(5)
+    layer = GraphTransformerLayer(64, 2, 8, 136, 4, axes=2, device=dev)
+    offsets = wl.offsets_from_sizes([200, 90]).to(dev)
+    x = torch.randn(290, 64, device=dev).to(BF).requires_grad_(True)
+    pos = torch.rand(290, 2, device=dev)
+    gy = torch.randn(290, 64, device=dev).to(BF)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            torch.autograd.grad(layer(x, offsets, pos), [x, layer.ffn.gate], gy)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer(x, offsets, pos)
+        dx, dgate = torch.autograd.grad(y, [x, layer.ffn.gate], gy)
+    with torch.no_grad():
+        x.mul_(0.75)
+    graph.replay()
+    torch.cuda.synchronize()
+    y2 = layer(x, offsets, pos)
+    dx2, dgate2 = torch.autograd.grad(y2, [x, layer.ffn.gate], gy)
+    torch.cuda.synchronize()
+    binding.check_status()
+    assert torch.equal(y, y2)
+    # dK and dV are fp32 atomic sums whose last bits vary
+    assert (dx.float() - dx2.float()).norm() <= 4e-3 * dx2.float().norm()
+    assert torch.equal(dgate, dgate2)
