@@ -60,10 +60,10 @@ extern "C" __attribute__((visibility("default"))) kmip_status_t kmip_ffn_fwd(
     if (e == cudaSuccess)
       e = launch_ffn_down(a, scratch, y, static_cast<char*>(scratch) + mat, stream);
   } else {
-    e = scratch_alloc(&scratch, 8 * nf + ffn_f32_scratch(), stream);
+    e = scratch_alloc(&scratch, 4 * nf + ffn_f32_scratch(), stream);
     if (e != cudaSuccess) return to_status(e);
-    float* ab = static_cast<float*>(scratch);
-    e = launch_ffn_f32_fwd(a, ab, static_cast<float*>(y), ab + 2 * nf, stream);
+    float* h = static_cast<float*>(scratch);
+    e = launch_ffn_f32_fwd(a, h, static_cast<float*>(y), h + nf, stream);
   }
   const cudaError_t ef = cudaFreeAsync(scratch, stream);
   return to_status(e != cudaSuccess ? e : ef);

@@ -37,10 +37,10 @@ constexpr int kFfnFewRows = 16;
 cudaError_t launch_ffn_rows_fwd(kmip_dtype_t dtype, const FfnArgs& a, float* h, void* y,
                                 cudaStream_t stream);
 
-// fp32 kernels (kmip_ffn_f32.cu); C and F multiples of 4.  ab: [2][N, F],
-// abd: [3][N, F], part: ffn_f32_scratch() bytes, all scratch.
+// fp32 kernels (kmip_ffn_f32.cu); C and F multiples of 4.  h: [N, F], abd:
+// [3][N, F], part: ffn_f32_scratch() bytes, all scratch.
 size_t ffn_f32_scratch();
-cudaError_t launch_ffn_f32_fwd(const FfnArgs& a, float* ab, float* y, float* part,
+cudaError_t launch_ffn_f32_fwd(const FfnArgs& a, float* h, float* y, float* part,
                                cudaStream_t stream);
 cudaError_t launch_ffn_f32_bwd(const FfnArgs& a, const float* dy, float* abd, float* dx,
                                float* dwg, float* dwu, float* dwd, float* part,

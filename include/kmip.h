@@ -353,8 +353,8 @@ kmip_status_t kmip_group_norm_bwd(const void* dy, const void* x, const void* wei
  * bf16 runs on the tcgen05 tensor cores with fp32 accumulation (the product
  * h of the two projections is rounded to bf16 between the GEMMs); fp32, and
  * up to 16 rows of either type, run on fp32 fused multiply-adds (few rows are
- * bound by reading the weights).  Takes N F elements of scratch (fp32: 2 N F;
- * up to 16 rows: N F fp32).
+ * bound by reading the weights).  Takes N F elements of scratch (up to 16
+ * rows: fp32 ones).
  * Supported: C and F multiples of 8, 8 .. 65536; all pointers 16-byte
  * aligned; y may not overlap an input.
  */
