@@ -359,16 +359,20 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _launch(x, name, stream, args, tail):
+def _launch(x, name, stream, args, tail, *used):
     """Calls entry point `name` with args, the stream and tail, with x's
     device current: on `stream`, or on that device's current stream.  Raises
-    on a status."""
+    on a status.  `used` (and x): the call's tensors, which torch's allocator
+    is told of when the call goes to a stream that is not theirs."""
     dev = x.get_device()
     if dev != _device():
         with torch.cuda.device(dev):
-            return _launch(x, name, stream, args, tail)
+            return _launch(x, name, stream, args, tail, *used)
     if stream is not None:
         s = stream.cuda_stream
+        for t in (x, *used):
+            if t is not None:
+                t.record_stream(stream)
     elif _raw_stream is not None:
         s = _raw_stream(dev)
     else:
@@ -409,7 +413,7 @@ def rotary(x, pos, freq, axis, inverse: bool = False, interleaved: bool = False,
     _launch(x, "kmip_rotary", stream,
             (x.data_ptr(), xs[0], xs[1], pos.data_ptr(), pos_type, pos.shape[1], freq.data_ptr(),
              axis.data_ptr(), P, bool(interleaved), bool(inverse), N, H, d, out.data_ptr(), os[0],
-             os[1]), (dtype_code(x.dtype),))
+             os[1]), (dtype_code(x.dtype),), pos, freq, axis, out)
     return out
 
 
@@ -433,7 +437,7 @@ def group_norm_fwd(x, weight, bias, groups: int, eps: float = 1e-5, act: str = "
     _launch(x, "kmip_group_norm_fwd", stream,
             (x.data_ptr(), _addr(weight), _addr(bias), _addr(graph_offsets), N, C, groups, eps,
              _act_code(act), y.data_ptr(), mean.data_ptr(), rstd.data_ptr()),
-            (G, dtype_code(x.dtype)))
+            (G, dtype_code(x.dtype)), weight, bias, graph_offsets, y, mean, rstd)
     return y, mean, rstd
 
 
@@ -458,7 +462,8 @@ def group_norm_bwd(dy, x, weight, bias, mean, rstd, groups: int, act: str = "non
     _launch(x, "kmip_group_norm_bwd", stream,
             (dy.data_ptr(), x.data_ptr(), _addr(weight), _addr(bias), _addr(graph_offsets),
              mean.data_ptr(), rstd.data_ptr(), N, C, groups, _act_code(act), dx.data_ptr(),
-             _addr(dw), _addr(db)), (G, dtype_code(x.dtype)))
+             _addr(dw), _addr(db)), (G, dtype_code(x.dtype)), dy, weight, bias, graph_offsets,
+            mean, rstd, dx, dw, db)
     return dx, dw, db
 
 
@@ -480,7 +485,7 @@ def ffn_fwd(x, wg, wu, wd, act: str = "silu", stream=None):
     y = torch.empty_like(x)
     _launch(x, "kmip_ffn_fwd", stream,
             (x.data_ptr(), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(), N, C, F, _act_code(act),
-             y.data_ptr()), (dtype_code(x.dtype),))
+             y.data_ptr()), (dtype_code(x.dtype),), wg, wu, wd, y)
     return y
 
 
@@ -494,7 +499,7 @@ def ffn_bwd(dy, x, wg, wu, wd, act: str = "silu", stream=None):
     _launch(x, "kmip_ffn_bwd", stream,
             (dy.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(), N, C, F,
              _act_code(act), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr()),
-            (dtype_code(x.dtype),))
+            (dtype_code(x.dtype),), dy, wg, wu, wd, dx, dwg, dwu, dwd)
     return dx, dwg, dwu, dwd
 
 

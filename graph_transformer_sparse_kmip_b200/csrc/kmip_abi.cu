@@ -374,4 +374,4 @@ KMIP_EXPORT int kmip_fwd_path(int d, int k, kmip_dtype_t dtype) {
   return dtype == KMIP_BF16 && fwd_tc_supported(d, k) ? 1 : 0;
 }
 
-KMIP_EXPORT int kmip_version(void) { return 200; }
+KMIP_EXPORT int kmip_version(void) { return 300; }

@@ -13,7 +13,9 @@ def dev():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
     binding.load()
-    return torch.device("cuda:0")
+    yield torch.device("cuda:0")
+    torch.cuda.synchronize()
+    binding.kmip_scratch_trim()  # other tests measure what the pool holds
 
 
 def test_attention_calls_can_be_captured(dev):
