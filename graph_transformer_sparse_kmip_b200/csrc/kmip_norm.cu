@@ -6,11 +6,14 @@
 namespace kmip {
 namespace {
 
-constexpr int kSplitThreads = 256, kSplitBlocks = 4;  // resident blocks of an SM
+// Threads of a split block: 256, or 384 where single elements or pairs of a row
+// fill more of those (345 channels: 345 of 384, not 253 and 92 of 256 each).
+constexpr int kSplitThreads = 256, kWideThreads = 384;
+// Blocks that can be resident on an SM, by registers.
+constexpr int split_blocks(int nt) { return nt == kSplitThreads ? 4 : 2; }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kSplitThreads, 4) norm_stats_split(const NormParams p) {
-  constexpr int NT = kSplitThreads;
+template <typename T, int V, int NT>
+__global__ void __launch_bounds__(NT, split_blocks(NT)) norm_stats_split(const NormParams p) {
   __shared__ StatSmem<NT> sm;
   const Slab s = make_slab<NT, V>(p, blockIdx.y);
   for (int slot = blockIdx.x; slot < p.slots; slot += gridDim.x) {
@@ -63,10 +66,10 @@ __global__ void __launch_bounds__(256) norm_join_stats(const NormParams p) {
   }
 }
 
-template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kSplitThreads, 4) norm_apply_split(const NormParams p) {
+template <typename T, int V, int ACT, int NT>
+__global__ void __launch_bounds__(NT, split_blocks(NT)) norm_apply_split(const NormParams p) {
   __shared__ float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
-  const Slab s = make_slab<kSplitThreads, V>(p, blockIdx.y);
+  const Slab s = make_slab<NT, V>(p, blockIdx.y);
   for (int slot = p.slots - 1 - (int)blockIdx.x; slot >= 0; slot -= gridDim.x) {
     int g, r0, r1;
     if (!slot_rows(p, slot, g, r0, r1)) continue;
@@ -77,9 +80,9 @@ __global__ void __launch_bounds__(kSplitThreads, 4) norm_apply_split(const NormP
   }
 }
 
-template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kSplitThreads, 3) norm_bwd_sums_split(const NormParams p) {
-  constexpr int NT = kSplitThreads;
+template <typename T, int V, int ACT, int NT>
+__global__ void __launch_bounds__(NT, NT == kSplitThreads ? 3 : 2)
+norm_bwd_sums_split(const NormParams p) {
   extern __shared__ float4 dyn[];
   BwdSmem<NT, V>& sm = *reinterpret_cast<BwdSmem<NT, V>*>(dyn);
   __shared__ float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
@@ -148,11 +151,12 @@ __global__ void __launch_bounds__(1024) norm_join_params(const float* src, int r
   }
 }
 
-template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kSplitThreads, 3) norm_bwd_apply_split(const NormParams p) {
+template <typename T, int V, int ACT, int NT>
+__global__ void __launch_bounds__(NT, NT == kSplitThreads ? 3 : 2)
+norm_bwd_apply_split(const NormParams p) {
   __shared__ float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
   __shared__ float m1[kMaxSlabGroups], m2[kMaxSlabGroups];
-  const Slab s = make_slab<kSplitThreads, V>(p, blockIdx.y);
+  const Slab s = make_slab<NT, V>(p, blockIdx.y);
   int have = -1;
   for (int slot = p.slots - 1 - (int)blockIdx.x; slot >= 0; slot -= gridDim.x) {
     int g, r0, r1;
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(kSplitThreads, 3) norm_bwd_apply_split(const N
       graph_rows(p, g, lo, hi);
       const float* src = p.gchan + (int64_t)g * 2 * p.C;
       const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-      for (int j = warp; j < s.ngroups; j += kSplitThreads / 32) {
+      for (int j = warp; j < s.ngroups; j += NT / 32) {
         double a = 0.0, b = 0.0;
         for (int c = lane; c < p.cg; c += 32) {
           const int ch = s.c0 + j * p.cg + c;
@@ -200,6 +204,7 @@ constexpr int64_t kOnceBytes = 64 << 20;
 struct Plan {
   bool resident;
   int slabs;
+  int nt;  // threads of a split block
 };
 
 // Sets p.gps, p.R, p.slots, p.once.
@@ -217,21 +222,43 @@ Plan plan(NormParams& p, int V, size_t esize) {
   int gps = slab_groups(64);
   if ((int64_t)p.G * ((p.groups + gps - 1) / gps) < sms) gps = slab_groups(32);
   pl.resident = row * p.N <= kResidentBytes && gps * group * (p.N / p.G) <= kResidentSlabBytes;
-  if (!pl.resident) {
-    // as many groups as a row of threads covers
-    gps = kSplitThreads * V / p.cg;
-    gps = gps < 1 ? 1 : gps > kMaxSlabGroups ? kMaxSlabGroups : gps;
-    gps = gps > p.groups ? p.groups : gps;
-  }
+  pl.nt = kSplitThreads;
   p.gps = gps;
-  pl.slabs = (p.groups + gps - 1) / gps;
+  if (!pl.resident) {
+    // even slabs of as many groups as a row of threads covers, with the
+    // number of threads that leaves fewer of them idle
+    double best = -1.0;
+    for (int nt : {kSplitThreads, kWideThreads}) {
+      if (nt != kSplitThreads && V > 2) break;
+      int64_t most = (int64_t)nt * V / p.cg;
+      most = most < 1 ? 1 : most > kMaxSlabGroups ? kMaxSlabGroups : most;
+      const int64_t slabs = (p.groups + most - 1) / most, even = (p.groups + slabs - 1) / slabs;
+      const int64_t vecs = even * p.cg / V, w = vecs < nt ? vecs : nt;
+      const int64_t rounds = (vecs + w - 1) / w;  // column tiles of a slab
+      const double used = (double)p.groups * p.cg / V * (nt / w) / ((double)slabs * rounds * nt);
+      if (used > best + 0.05) {
+        best = used;
+        pl.nt = nt;
+        p.gps = (int)even;
+      }
+    }
+  }
+  pl.slabs = (p.groups + p.gps - 1) / p.gps;
   // one slot for every block that can be resident, of at least 64 rows
-  const int64_t want = (int64_t)sms * kSplitBlocks;
+  const int64_t want = (int64_t)sms * split_blocks(pl.nt);
   const int64_t R = ((int64_t)p.N * pl.slabs + want - 1) / want;
   p.R = (int)(R < 64 ? 64 : R);
   p.slots = p.N / p.R + p.G;
   p.once = row * p.N > kOnceBytes;
   return pl;
+}
+
+template <int V, typename F>
+cudaError_t with_threads(int nt, F&& f) {
+  if constexpr (V <= 2) {
+    if (nt == kWideThreads) return f.template operator()<kWideThreads>();
+  }
+  return f.template operator()<kSplitThreads>();
 }
 
 dim3 split_grid(const NormParams& p, int slabs) {
@@ -249,11 +276,13 @@ cudaError_t norm_fwd(kmip_dtype_t dtype, int v, int act, NormParams p, cudaStrea
   p.part = static_cast<double2*>(scratch);
   const dim3 grid = split_grid(p, pl.slabs);
   e = norm_dispatch(dtype, v, act, [&]<typename T, int V, int ACT>() {
-    norm_stats_split<T, V><<<grid, kSplitThreads, 0, stream>>>(p);
-    const int64_t joins = (int64_t)p.G * p.groups;
-    norm_join_stats<<<(unsigned)(joins < 65536 ? joins : 65536), 256, 0, stream>>>(p);
-    norm_apply_split<T, V, ACT><<<grid, kSplitThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return with_threads<V>(pl.nt, [&]<int NT>() {
+      norm_stats_split<T, V, NT><<<grid, NT, 0, stream>>>(p);
+      const int64_t joins = (int64_t)p.G * p.groups;
+      norm_join_stats<<<(unsigned)(joins < 65536 ? joins : 65536), 256, 0, stream>>>(p);
+      norm_apply_split<T, V, ACT, NT><<<grid, NT, 0, stream>>>(p);
+      return cudaGetLastError();
+    });
   });
   const cudaError_t ef = cudaFreeAsync(scratch, stream);
   return e != cudaSuccess ? e : ef;
@@ -283,11 +312,14 @@ cudaError_t norm_bwd(kmip_dtype_t dtype, int v, int act, NormParams p, void* dwe
         float* gchan = p.chan + rows * cols;
         const bool direct = params && p.G == 1;
         p.gchan = gchan;
-        norm_bwd_sums_split<T, V, ACT>
-            <<<grid, kSplitThreads, sizeof(BwdSmem<kSplitThreads, V>), stream>>>(p);
-        norm_join_graph<T><<<dim3(tiles, p.G < 65535 ? p.G : 65535), 1024, 0, stream>>>(
-            p, gchan, direct ? dw : nullptr, db);
-        norm_bwd_apply_split<T, V, ACT><<<grid, kSplitThreads, 0, stream>>>(p);
+        const cudaError_t el = with_threads<V>(pl.nt, [&]<int NT>() {
+          norm_bwd_sums_split<T, V, ACT, NT><<<grid, NT, sizeof(BwdSmem<NT, V>), stream>>>(p);
+          norm_join_graph<T><<<dim3(tiles, p.G < 65535 ? p.G : 65535), 1024, 0, stream>>>(
+              p, gchan, direct ? dw : nullptr, db);
+          norm_bwd_apply_split<T, V, ACT, NT><<<grid, NT, 0, stream>>>(p);
+          return cudaGetLastError();
+        });
+        if (el != cudaSuccess) return el;
         sums = gchan;
         nsums = p.G;
         params = params && !direct;

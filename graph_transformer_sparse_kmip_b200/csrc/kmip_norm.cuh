@@ -25,10 +25,9 @@
 //             reverse order, so that what the first pass left in L2 is met
 //             first.  Any graph size spreads over all SMs.
 //
-// Statistics that are not held: a thread takes kRows x V values at a time,
-// forms their own mean and squared deviations (two passes over registers) and
-// joins them to its running (n, mean, M2); no difference of large sums is
-// formed in fp32.  Threads, and blocks, join in fp64 sums of n mean and
+// Statistics that are not held: a thread keeps (n, mean, M2) and adds kRows x V
+// values at a time by their deviations from its mean; no difference of large
+// sums is formed in fp32.  Threads, and blocks, join in fp64 sums of n mean and
 // M2 + n mean^2.  All sums run in a fixed order: no atomics, the same bits
 // every run.
 #pragma once
@@ -72,33 +71,36 @@ struct Row {
   R raw;
   __device__ void load(const T* p) { raw = *reinterpret_cast<const R*>(p); }
   __device__ void load_last(const T* p) { raw = __ldcs(reinterpret_cast<const R*>(p)); }
-  __device__ void get(float (&f)[V]) const {
+  // As pairs (P = 1 single, in .x, when V = 1).
+  static constexpr int P = V > 1 ? V / 2 : 1;
+  __device__ void get(float2 (&f)[P]) const {
     if constexpr (sizeof(T) == 4) {
       const float* q = reinterpret_cast<const float*>(&raw);
 #pragma unroll
-      for (int e = 0; e < V; ++e) f[e] = q[e];
+      for (int e = 0; e < P; ++e) f[e] = make_float2(q[V > 1 ? 2 * e : 0], V > 1 ? q[2 * e + 1] : 0.f);
     } else if constexpr (V == 1) {
-      f[0] = __uint_as_float((uint32_t)raw << 16);
+      f[0] = make_float2(__uint_as_float((uint32_t)raw << 16), 0.f);
     } else {
       const uint32_t* q = reinterpret_cast<const uint32_t*>(&raw);
 #pragma unroll
-      for (int e = 0; e < V / 2; ++e) {
-        f[2 * e] = __uint_as_float(q[e] << 16);
-        f[2 * e + 1] = __uint_as_float(q[e] & 0xffff0000u);
-      }
+      for (int e = 0; e < P; ++e)
+        f[e] = make_float2(__uint_as_float(q[e] << 16), __uint_as_float(q[e] & 0xffff0000u));
     }
   }
-  __device__ void set(const float (&f)[V]) {
+  __device__ void set(const float2 (&f)[P]) {
     if constexpr (sizeof(T) == 4) {
       float* q = reinterpret_cast<float*>(&raw);
 #pragma unroll
-      for (int e = 0; e < V; ++e) q[e] = f[e];
+      for (int e = 0; e < P; ++e) {
+        q[V > 1 ? 2 * e : 0] = f[e].x;
+        if (V > 1) q[2 * e + 1] = f[e].y;
+      }
     } else if constexpr (V == 1) {
-      raw = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+      raw = __bfloat16_as_ushort(__float2bfloat16_rn(f[0].x));
     } else {
       __nv_bfloat162* q = reinterpret_cast<__nv_bfloat162*>(&raw);
 #pragma unroll
-      for (int e = 0; e < V / 2; ++e) q[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+      for (int e = 0; e < P; ++e) q[e] = __floats2bfloat162_rn(f[e].x, f[e].y);
     }
   }
   __device__ void store(T* p, int once) const {
@@ -106,6 +108,20 @@ struct Row {
     else *reinterpret_cast<R*>(p) = raw;
   }
 };
+
+// Pairs of V elements; with V = 1 only .x counts, and plain instructions serve.
+template <int V>
+__device__ __forceinline__ float2 vadd(float2 a, float2 b) {
+  return V > 1 ? add2(a, b) : make_float2(a.x + b.x, 0.f);
+}
+template <int V>
+__device__ __forceinline__ float2 vmul(float2 a, float2 b) {
+  return V > 1 ? mul2(a, b) : make_float2(a.x * b.x, 0.f);
+}
+template <int V>
+__device__ __forceinline__ float2 vfma(float2 a, float2 b, float2 c) {
+  return V > 1 ? fma2(a, b, c) : make_float2(fmaf(a.x, b.x, c.x), 0.f);
+}
 
 // ---------------------------------------------------------------- row ranges
 // Node range of graph g; false (and a status) when its offsets are malformed.
@@ -163,11 +179,13 @@ __device__ __forceinline__ Slab make_slab(const NormParams& p, int slab) {
   return s;
 }
 
-// Batches of the split kernels' passes over x, and over x and dy.
+// Rows of a batch in the split kernels' passes over x, and over x and dy: 64
+// bytes of each thread on their way twice over (31,623 x 345 fp32 training
+// step, single elements: 110 us with half of that, 97 with this).
 template <int V>
-constexpr int kRowsOne = V >= 4 ? 4 : 8;
+constexpr int kRowsOne = V >= 4 ? 4 : 16;
 template <int V>
-constexpr int kRowsTwo = V >= 4 ? 2 : 4;
+constexpr int kRowsTwo = V >= 4 ? 2 : 8;
 
 // Rows r0 + ty, + TY, ... of a column in batches of KR: body(rows, r, n) with
 // the n <= KR rows r, r + TY, ..., the next batch already on its way.
@@ -202,6 +220,20 @@ __device__ __forceinline__ void walk_rows(const Slab& s, int r0, int r1, int64_t
   }
 }
 
+// Adds x - shift and its square over a row's vector.
+template <typename T, int V>
+__device__ __forceinline__ void add_deviations(const Row<T, V>& row, float shift, float2& sum,
+                                               float2& square) {
+  float2 f[Row<T, V>::P];
+  row.get(f);
+#pragma unroll
+  for (int e = 0; e < Row<T, V>::P; ++e) {
+    const float2 t = vadd<V>(f[e], make_float2(-shift, V > 1 ? -shift : 0.f));
+    sum = vadd<V>(sum, t);
+    square = vfma<V>(t, t, square);
+  }
+}
+
 template <int NT>
 struct StatSmem {
   double s0[NT], q[NT];
@@ -220,33 +252,25 @@ __device__ void slab_stats(const NormParams& p, const Slab& s, int r0, int r1,
     if (s.ty < s.TY && v < s.vecs) {
       const T* const cols[1] = {static_cast<const T*>(p.x) + s.c0 + v * V};
       walk_rows<KR, T, V, 1>(s, r0, r1, p.C, cols, false, [&](Row<T, V> (&rows)[1][KR], int r) {
-        const int cnt = min((r1 - r + s.TY - 1) / s.TY, KR);
-        float sum = 0.f, dev = 0.f;
+        // squared deviations from the running mean (at first from one of the
+        // values): sum d^2 - (sum d)^2 / n is then a difference of like terms
+        // only where it is large itself
+        if (n == 0.f) {
+          float2 f[Row<T, V>::P];
+          rows[0][0].get(f);
+          mean = f[0].x;
+        }
+        float2 sum = make_float2(0.f, 0.f), dev = sum;
+        int cnt = 0;
 #pragma unroll
         for (int u = 0; u < KR; ++u)
-          if (u < cnt) {
-            float f[V];
-            rows[0][u].get(f);
-#pragma unroll
-            for (int e = 0; e < V; ++e) sum += f[e];
+          if (r + u * s.TY < r1) {
+            add_deviations<T, V>(rows[0][u], mean, sum, dev);
+            ++cnt;
           }
-        const float nb = (float)(cnt * V);
-        const float mb = __fdividef(sum, nb);
-#pragma unroll
-        for (int u = 0; u < KR; ++u)
-          if (u < cnt) {
-            float f[V];
-            rows[0][u].get(f);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              const float t = f[e] - mb;
-              dev = fmaf(t, t, dev);
-            }
-          }
-        // (mb is the mean up to rounding, which the join takes as it is)
-        const float all = n + nb, d = mb - mean, share = __fdividef(nb, all);
-        mean = fmaf(d, share, mean);
-        m2 += fmaf(d * d, n * share, dev);
+        const float all = n + (float)(cnt * V), d = sum.x + sum.y, share = __fdividef(d, all);
+        mean += share;
+        m2 += fmaf(-d, share, dev.x + dev.y);
         n = all;
       });
     }
@@ -288,65 +312,100 @@ __device__ __forceinline__ void finish_stats(double s0, double q, double count, 
   rstd = (float)rsqrt(var + (double)eps);
 }
 
-// Channel parameters of a vector, as they are stored.
+// Weight and bias of a vector.
 template <typename T, int V>
-struct Affine {
-  Row<T, V> w, b;
-  __device__ void load(const NormParams& p, int c) {
-    if (p.w) {
-      w.load(static_cast<const T*>(p.w) + c);
-      b.load(static_cast<const T*>(p.b) + c);
-    } else {
-      float one[V], zero[V];
+__device__ __forceinline__ void load_affine(const NormParams& p, int c,
+                                            float2 (&w)[Row<T, V>::P], float2 (&b)[Row<T, V>::P]) {
+  if (p.w) {
+    Row<T, V> r;
+    r.load(static_cast<const T*>(p.w) + c);
+    r.get(w);
+    r.load(static_cast<const T*>(p.b) + c);
+    r.get(b);
+  } else {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        one[e] = 1.f;
-        zero[e] = 0.f;
-      }
-      w.set(one);
-      b.set(zero);
+    for (int e = 0; e < Row<T, V>::P; ++e) {
+      w[e] = splat2(1.f);
+      b[e] = splat2(0.f);
     }
+  }
+}
+
+// z = x a + c for bf16, whose inputs carry 2^-9 of x already (the product's
+// rounding is 2^-24 of x rstd w); (x - mean) a + c for fp32, which takes the
+// difference first.
+template <typename T, int V>
+struct Forward {
+  static constexpr int P = Row<T, V>::P;
+  float2 a[P], c[P];
+  float mean;
+  __device__ void set(const NormParams& p, int ch, float m, float rs) {
+    load_affine<T, V>(p, ch, a, c);
+    mean = m;
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      a[e] = vmul<V>(a[e], splat2(rs));
+      if (sizeof(T) == 2) c[e] = vfma<V>(a[e], splat2(-m), c[e]);
+    }
+  }
+  template <int ACT>
+  __device__ void apply(Row<T, V>& row) const {
+    float2 f[P];
+    row.get(f);
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      if (sizeof(T) == 4) f[e] = vadd<V>(f[e], splat2(-mean));
+      const float2 z = vfma<V>(f[e], a[e], c[e]);
+      f[e] = V > 1 ? act_value2<T, ACT>(z) : make_float2(act_value<T, ACT>(z.x), 0.f);
+    }
+    row.set(f);
   }
 };
 
-// xhat of one element.  bf16 inputs carry 2^-9 of x already, so one fused
-// multiply-add (2^-24 of x rstd) will do; fp32 takes the difference first.
-template <typename T>
-__device__ __forceinline__ float normed(float x, float m, float rs) {
-  return sizeof(T) == 2 ? fmaf(x, rs, -m * rs) : (x - m) * rs;
-}
-
-// y of one vector.
-template <typename T, int V, int ACT>
-__device__ __forceinline__ void row_fwd(Row<T, V>& row, float m, float rs,
-                                        const Affine<T, V>& af) {
-  float f[V], w[V], b[V];
-  row.get(f);
-  af.w.get(w);
-  af.b.get(b);
-#pragma unroll
-  for (int e = 0; e < V; ++e) f[e] = act_value<T, ACT>(fmaf(normed<T>(f[e], m, rs), w[e], b[e]));
-  row.set(f);
-}
-
-// xhat, dz and the weights of one vector.
-template <typename T, int V, int ACT>
-__device__ __forceinline__ void row_bwd(const Row<T, V>& row, const Row<T, V>& grad, float m,
-                                        float rs, const Affine<T, V>& af, float (&xh)[V],
-                                        float (&dz)[V], float (&w)[V]) {
-  float b[V];
-  row.get(xh);
-  grad.get(dz);
-  af.w.get(w);
-  af.b.get(b);
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    float fa, ga;
-    xh[e] = normed<T>(xh[e], m, rs);
-    act_both<T, ACT>(fmaf(xh[e], w[e], b[e]), fa, ga);
-    dz[e] *= ga;
+// xhat and dz of a vector, likewise.
+template <typename T, int V>
+struct Backward {
+  static constexpr int P = Row<T, V>::P;
+  float2 w[P], b[P];
+  float mean, rs;
+  __device__ void set(const NormParams& p, int ch, float m, float r) {
+    load_affine<T, V>(p, ch, w, b);
+    mean = m;
+    rs = r;
   }
-}
+  template <int ACT>
+  __device__ void rows(const Row<T, V>& row, const Row<T, V>& grad, float2 (&xh)[P],
+                       float2 (&dz)[P]) const {
+    row.get(xh);
+    grad.get(dz);
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      xh[e] = sizeof(T) == 2 ? vfma<V>(xh[e], splat2(rs), splat2(-mean * rs))
+                             : vmul<V>(vadd<V>(xh[e], splat2(-mean)), splat2(rs));
+      const float2 z = vfma<V>(xh[e], w[e], b[e]);
+      float2 f, g;
+      if (V > 1) {
+        act_both2<T, ACT>(z, f, g);
+      } else {
+        act_both<T, ACT>(z.x, f.x, g.x);
+        g.y = 0.f;
+      }
+      dz[e] = vmul<V>(dz[e], g);
+    }
+  }
+  // dx = rs (dz w - m1 - xhat m2), into grad's place
+  template <int ACT>
+  __device__ void apply(const Row<T, V>& row, Row<T, V>& grad, float m1, float m2) const {
+    float2 xh[P], dz[P];
+    rows<ACT>(row, grad, xh, dz);
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      const float2 t = vfma<V>(dz[e], w[e], splat2(-m1));
+      dz[e] = vmul<V>(vfma<V>(xh[e], splat2(-m2), t), splat2(rs));
+    }
+    grad.set(dz);
+  }
+};
 
 template <typename T, int V, int ACT, int KR>
 __device__ void slab_apply(const NormParams& p, const Slab& s, int r0, int r1, const float* mean,
@@ -354,16 +413,15 @@ __device__ void slab_apply(const NormParams& p, const Slab& s, int r0, int r1, c
   if (s.ty >= s.TY) return;
   for (int v = s.tx; v < s.vecs; v += s.W) {
     const int c = s.c0 + v * V, j = v * V / p.cg;
-    Affine<T, V> af;
-    af.load(p, c);
-    const float m = mean[j], rs = rstd[j];
+    Forward<T, V> fw;
+    fw.set(p, c, mean[j], rstd[j]);
     const T* const cols[1] = {static_cast<const T*>(p.x) + c};
     T* out = static_cast<T*>(p.y) + c;
     walk_rows<KR, T, V, 1>(s, r0, r1, p.C, cols, p.once, [&](Row<T, V> (&rows)[1][KR], int r) {
 #pragma unroll
       for (int u = 0; u < KR; ++u)
         if (r + u * s.TY < r1) {
-          row_fwd<T, V, ACT>(rows[0][u], m, rs, af);
+          fw.template apply<ACT>(rows[0][u]);
           rows[0][u].store(out + (int64_t)(r + u * s.TY) * p.C, p.once);
         }
     });
@@ -384,14 +442,15 @@ struct BwdSmem {
 // slab): sdb, sdw of each thread, over ty, to dst[0][c], dst[1][c] (added to
 // what is there unless `first`); with GROUPS also added to sm.gm1, sm.gm2.
 template <typename T, int V, int NT, bool GROUPS>
-__device__ void join_channels(const NormParams& p, const Slab& s, int vt, const float (&sdb)[V],
-                              const float (&sdw)[V], float* dst, bool first, BwdSmem<NT, V>& sm) {
+__device__ void join_channels(const NormParams& p, const Slab& s, int vt,
+                              const float2 (&sdb)[Row<T, V>::P], const float2 (&sdw)[Row<T, V>::P],
+                              float* dst, bool first, BwdSmem<NT, V>& sm) {
   const int pitch = s.TY | 1, tile = min(s.W, s.vecs - vt) * V;
   if (s.ty < s.TY) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      sm.red[0][(s.tx * V + e) * pitch + s.ty] = sdb[e];
-      sm.red[1][(s.tx * V + e) * pitch + s.ty] = sdw[e];
+      sm.red[0][(s.tx * V + e) * pitch + s.ty] = e & 1 ? sdb[e / 2].y : sdb[e / 2].x;
+      sm.red[1][(s.tx * V + e) * pitch + s.ty] = e & 1 ? sdw[e / 2].y : sdw[e / 2].x;
     }
   }
   __syncthreads();
@@ -453,25 +512,25 @@ __device__ void slab_bwd_sums(const NormParams& p, const Slab& s, int r0, int r1
                               BwdSmem<NT, V>& sm) {
   for (int vt = 0; vt < s.vecs; vt += s.W) {
     const int v = vt + s.tx;
-    float sdb[V], sdw[V];
+    constexpr int P = Row<T, V>::P;
+    float2 sdb[P], sdw[P];
 #pragma unroll
-    for (int e = 0; e < V; ++e) sdb[e] = sdw[e] = 0.f;
+    for (int e = 0; e < P; ++e) sdb[e] = sdw[e] = splat2(0.f);
     if (s.ty < s.TY && v < s.vecs) {
       const int c = s.c0 + v * V, j = v * V / p.cg;
-      Affine<T, V> af;
-      af.load(p, c);
-      const float m = mean[j], rs = rstd[j];
+      Backward<T, V> bw;
+      bw.set(p, c, mean[j], rstd[j]);
       const T* const cols[2] = {static_cast<const T*>(p.x) + c, static_cast<const T*>(p.dy) + c};
       walk_rows<KR, T, V, 2>(s, r0, r1, p.C, cols, false, [&](Row<T, V> (&rows)[2][KR], int r) {
 #pragma unroll
         for (int u = 0; u < KR; ++u)
           if (r + u * s.TY < r1) {
-            float xh[V], dz[V], w[V];
-            row_bwd<T, V, ACT>(rows[0][u], rows[1][u], m, rs, af, xh, dz, w);
+            float2 xh[P], dz[P];
+            bw.template rows<ACT>(rows[0][u], rows[1][u], xh, dz);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              sdb[e] += dz[e];
-              sdw[e] = fmaf(dz[e], xh[e], sdw[e]);
+            for (int e = 0; e < P; ++e) {
+              sdb[e] = vadd<V>(sdb[e], dz[e]);
+              sdw[e] = vfma<V>(dz[e], xh[e], sdw[e]);
             }
           }
       });
@@ -487,20 +546,16 @@ __device__ void slab_bwd_apply(const NormParams& p, const Slab& s, int r0, int r
   if (s.ty >= s.TY) return;
   for (int v = s.tx; v < s.vecs; v += s.W) {
     const int c = s.c0 + v * V, j = v * V / p.cg;
-    Affine<T, V> af;
-    af.load(p, c);
-    const float m = mean[j], rs = rstd[j], a1 = m1[j], a2 = m2[j];
+    Backward<T, V> bw;
+    bw.set(p, c, mean[j], rstd[j]);
+    const float a1 = m1[j], a2 = m2[j];
     const T* const cols[2] = {static_cast<const T*>(p.x) + c, static_cast<const T*>(p.dy) + c};
     T* out = static_cast<T*>(p.dx) + c;
     walk_rows<KR, T, V, 2>(s, r0, r1, p.C, cols, p.once, [&](Row<T, V> (&rows)[2][KR], int r) {
 #pragma unroll
       for (int u = 0; u < KR; ++u)
         if (r + u * s.TY < r1) {
-          float xh[V], dz[V], w[V];
-          row_bwd<T, V, ACT>(rows[0][u], rows[1][u], m, rs, af, xh, dz, w);
-#pragma unroll
-          for (int e = 0; e < V; ++e) dz[e] = rs * (fmaf(dz[e], w[e], -a1) - xh[e] * a2);
-          rows[1][u].set(dz);
+          bw.template apply<ACT>(rows[0][u], rows[1][u], a1, a2);
           rows[1][u].store(out + (int64_t)(r + u * s.TY) * p.C, p.once);
         }
     });

@@ -54,7 +54,7 @@ __device__ __forceinline__ float group_sum(const NormParams& p, const Slab& s, f
 }
 
 template <typename T, int V, int ACT, int NT, int HOLD>
-__global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) norm_fwd_resident(const NormParams p) {
+__global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_fwd_resident(const NormParams p) {
   __shared__ StatSmem<NT> sm;
   const Slab s = make_slab<NT, V>(p, blockIdx.y);
   for (int g = blockIdx.x; g < p.G; g += gridDim.x) {
@@ -72,43 +72,31 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) norm_fwd_resident(const
 #pragma unroll
       for (int u = 0; u < HOLD; ++u)
         if (u * s.TY < mine) x[u].load(src + (first + u * step));
-      Affine<T, V> af;
-      af.load(p, c);
-      float sum = 0.f, dev = 0.f;
+      float2 sum = splat2(0.f), dev = sum;
 #pragma unroll
       for (int u = 0; u < HOLD; ++u)
-        if (u * s.TY < mine) {
-          float f[V];
-          x[u].get(f);
-#pragma unroll
-          for (int e = 0; e < V; ++e) sum += f[e];
-        }
+        if (u * s.TY < mine) add_deviations<T, V>(x[u], 0.f, sum, dev);
       const float count = (float)rows * (float)p.cg;
       float* v0 = reinterpret_cast<float*>(sm.s0);
       float* v1 = reinterpret_cast<float*>(sm.q);
-      const float m = group_sum<V, NT>(p, s, sum, v0, sm.mean) / count;
+      const float m = group_sum<V, NT>(p, s, sum.x + sum.y, v0, sm.mean) / count;
+      dev = sum = splat2(0.f);
 #pragma unroll
       for (int u = 0; u < HOLD; ++u)
-        if (u * s.TY < mine) {
-          float f[V];
-          x[u].get(f);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float t = f[e] - m;
-            dev = fmaf(t, t, dev);
-          }
-        }
-      const float var = group_sum<V, NT>(p, s, dev, v1, sm.rstd) / count;
+        if (u * s.TY < mine) add_deviations<T, V>(x[u], m, sum, dev);
+      const float var = group_sum<V, NT>(p, s, dev.x + dev.y, v1, sm.rstd) / count;
       const float rs = 1.f / sqrtf(var + p.eps);
       if (s.ty == 0 && s.tx * V % p.cg == 0) {
         p.mean[at + s.tx * V / p.cg] = m;
         p.rstd[at + s.tx * V / p.cg] = rs;
       }
+      Forward<T, V> fw;
+      fw.set(p, c, m, rs);
       T* out = static_cast<T*>(p.y);
 #pragma unroll
       for (int u = 0; u < HOLD; ++u)
         if (u * s.TY < mine) {
-          row_fwd<T, V, ACT>(x[u], m, rs, af);
+          fw.template apply<ACT>(x[u]);
           x[u].store(out + (first + u * step), 0);
         }
       __syncthreads();
@@ -155,23 +143,23 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_bwd_resident(const
           x[u].load(src + (first + u * step));
           dy[u].load(gsrc + (first + u * step));
         }
-      Affine<T, V> af;
-      af.load(p, c);
-      const float m = p.mean[(int64_t)g * p.groups + s.g0 + j];
-      const float rs = p.rstd[(int64_t)g * p.groups + s.g0 + j];
+      Backward<T, V> bw;
+      bw.set(p, c, p.mean[(int64_t)g * p.groups + s.g0 + j],
+             p.rstd[(int64_t)g * p.groups + s.g0 + j]);
       {
-        float sdb[V], sdw[V];
+        constexpr int P = Row<T, V>::P;
+        float2 sdb[P], sdw[P];
 #pragma unroll
-        for (int e = 0; e < V; ++e) sdb[e] = sdw[e] = 0.f;
+        for (int e = 0; e < P; ++e) sdb[e] = sdw[e] = splat2(0.f);
 #pragma unroll
         for (int u = 0; u < HOLD; ++u)
           if (u * s.TY < mine) {
-            float xh[V], dz[V], w[V];
-            row_bwd<T, V, ACT>(x[u], dy[u], m, rs, af, xh, dz, w);
+            float2 xh[P], dz[P];
+            bw.template rows<ACT>(x[u], dy[u], xh, dz);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              sdb[e] += dz[e];
-              sdw[e] = fmaf(dz[e], xh[e], sdw[e]);
+            for (int e = 0; e < P; ++e) {
+              sdb[e] = vadd<V>(sdb[e], dz[e]);
+              sdw[e] = vfma<V>(dz[e], xh[e], sdw[e]);
             }
           }
         join_channels<T, V, NT, true>(p, s, 0, sdb, sdw, dst, first_graph, sm);
@@ -183,11 +171,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_bwd_resident(const
 #pragma unroll
       for (int u = 0; u < HOLD; ++u)
         if (u * s.TY < mine) {
-          float xh[V], dz[V], w[V];
-          row_bwd<T, V, ACT>(x[u], dy[u], m, rs, af, xh, dz, w);
-#pragma unroll
-          for (int e = 0; e < V; ++e) dz[e] = rs * (fmaf(dz[e], w[e], -a1) - xh[e] * a2);
-          dy[u].set(dz);
+          bw.template apply<ACT>(x[u], dy[u], a1, a2);
           dy[u].store(out + (first + u * step), 0);
         }
       __syncthreads();
