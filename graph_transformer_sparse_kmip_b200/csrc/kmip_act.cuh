@@ -122,12 +122,20 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return as_f2(r);
 }
 
+// Sigmoids of two values, z limited from below to kLeast first (silu(kLeast) is
+// -5e-18; a NaN stays).  bf16: both quotients out of one reciprocal, of the
+// product of the denominators, which that limit keeps under 2^127: three
+// slow-pipe instructions for two values instead of four.
+constexpr float kLeast = -44.f;
 template <typename T>
-__device__ __forceinline__ float2 sigmoid2(float2 z) {
+__device__ __forceinline__ float2 sigmoid2(float2& z) {
   if constexpr (sizeof(T) == 2) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(z.x) : "f"(kLeast));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(z.y) : "f"(kLeast));
     const float2 t = mul2(z, splat2(-1.4426950408889634f));
     const float2 q = add2(make_float2(ex2_fast(t.x), ex2_fast(t.y)), splat2(1.f));
-    return make_float2(rcp_fast(q.x), rcp_fast(q.y));
+    const float r = rcp_fast(q.x * q.y);
+    return make_float2(q.y * r, q.x * r);
   } else {
     return make_float2(sigmoid<T>(z.x), sigmoid<T>(z.y));
   }
@@ -135,7 +143,10 @@ __device__ __forceinline__ float2 sigmoid2(float2 z) {
 
 template <typename T, int ACT>
 __device__ __forceinline__ float2 act_value2(float2 z) {
-  if constexpr (ACT == KMIP_ACT_SILU) return mul2(z, sigmoid2<T>(z));
+  if constexpr (ACT == KMIP_ACT_SILU) {
+    const float2 s = sigmoid2<T>(z);
+    return mul2(z, s);
+  }
   return make_float2(act_value<T, ACT>(z.x), act_value<T, ACT>(z.y));
 }
 

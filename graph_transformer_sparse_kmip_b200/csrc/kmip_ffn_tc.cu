@@ -145,6 +145,8 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ uint32_t pack2(float2 v) { return pack2(v.x, v.y); }
+
 template <int MODE, int BN, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
@@ -367,8 +369,8 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
           uint32_t w[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            w[e] = pack2(act_value<T, ACT>(g[2 * e]) * u[2 * e],
-                         act_value<T, ACT>(g[2 * e + 1]) * u[2 * e + 1]);
+            w[e] = pack2(mul2(act_value2<T, ACT>(make_float2(g[2 * e], g[2 * e + 1])),
+                              make_float2(u[2 * e], u[2 * e + 1])));
           if (c == 0) boxes_free();
           put_box(box, lane, c, w);
         }
@@ -391,18 +393,14 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
           uint32_t wa[8], wb[8], wh[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            float ra[2], rb[2], rh[2];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              float fa, ga;
-              act_both<T, ACT>(a[2 * e + z], fa, ga);
-              ra[z] = dh[2 * e + z] * b[2 * e + z] * ga;
-              rb[z] = dh[2 * e + z] * fa;
-              rh[z] = fa * b[2 * e + z];
-            }
-            wa[e] = pack2(ra[0], ra[1]);
-            wb[e] = pack2(rb[0], rb[1]);
-            wh[e] = pack2(rh[0], rh[1]);
+            const float2 av = make_float2(a[2 * e], a[2 * e + 1]);
+            const float2 bv = make_float2(b[2 * e], b[2 * e + 1]);
+            const float2 dv = make_float2(dh[2 * e], dh[2 * e + 1]);
+            float2 f, g;
+            act_both2<T, ACT>(av, f, g);
+            wa[e] = pack2(mul2(mul2(dv, bv), g));
+            wb[e] = pack2(mul2(dv, f));
+            wh[e] = pack2(mul2(f, bv));
           }
           if (c == 0) boxes_free();
           put_box(box, lane, c, wa);
