@@ -66,6 +66,25 @@ __global__ void __launch_bounds__(256) norm_join_stats(const NormParams p) {
   }
 }
 
+// The same for graphs of a few slots: one thread per (graph, group).
+__global__ void __launch_bounds__(256) norm_join_stats_few(const NormParams p) {
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < (int64_t)p.G * p.groups;
+       i += gridDim.x * 256ll) {
+    const int g = (int)(i / p.groups), j = (int)(i % p.groups);
+    int lo, hi;
+    if (!graph_rows(p, g, lo, hi)) continue;
+    const int a = first_slot(p, g), n = (int)(((int64_t)hi - lo + p.R - 1) / p.R);
+    double x = 0.0, q = 0.0;
+#pragma unroll 4
+    for (int t = 0; t < n; ++t) {
+      const double2 v = p.part[(int64_t)(a + t) * p.groups + j];
+      x += v.x;
+      q += v.y;
+    }
+    finish_stats(x, q, (double)(hi - lo) * p.cg, p.eps, p.mean[i], p.rstd[i]);
+  }
+}
+
 template <typename T, int V, int ACT, int NT>
 __global__ void __launch_bounds__(NT, split_blocks(NT)) norm_apply_split(const NormParams p) {
   __shared__ float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
@@ -138,6 +157,22 @@ __global__ void __launch_bounds__(1024) norm_join_graph(const NormParams p, floa
   }
 }
 
+// The same for graphs of a few slots: one warp per graph and 32 columns.
+__global__ void __launch_bounds__(256) norm_join_graph_few(const NormParams p, float* gchan) {
+  const int64_t cols = 2 * (int64_t)p.C, col = blockIdx.x * 32ll + (threadIdx.x & 31);
+  if (col >= cols) return;
+  for (int64_t g = blockIdx.y * 8ll + (threadIdx.x >> 5); g < p.G; g += gridDim.y * 8ll) {
+    int lo, hi;
+    if (!graph_rows(p, (int)g, lo, hi)) lo = hi = 0;
+    const int n = (int)(((int64_t)hi - lo + p.R - 1) / p.R);
+    const float* src = p.chan + (hi > lo ? (int64_t)first_slot(p, (int)g) * cols : 0) + col;
+    float a = 0.f;
+#pragma unroll 4
+    for (int r = 0; r < n; ++r) a += src[r * cols];
+    gchan[g * cols + col] = a;
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_join_params(const float* src, int rows, int C, T* dw,
                                                          T* db) {
@@ -196,8 +231,17 @@ norm_bwd_apply_split(const NormParams p) {
 
 // --------------------------------------------------------------------- host
 // Inputs up to this size, with graphs whose slab of one block is small, take
-// the resident kernels.
-constexpr int64_t kResidentBytes = 16 << 20, kResidentSlabBytes = 128 << 10;
+// the resident kernels (100,000 x 128 bf16 in 210 graphs: 16 us forward where the
+// split ones take 30; 200,000 x 128 in 10,000: 103 and 198).  Where groups allow
+// no wide loads the split ones win earlier (150,000 x 155 bf16 in 1,500 graphs:
+// 129 us resident, 112 split).
+constexpr int64_t kResidentBytes = 64 << 20, kResidentNarrowBytes = 16 << 20;
+constexpr int64_t kResidentSlabBytes = 128 << 10;
+// Bytes of a graph that a resident block should have to itself, if there are
+// as many: it spends 3 to 4 us on a graph apart from its rows.
+constexpr int64_t kResidentWorth = 16 << 10;
+// A block spends about 2 us on a slot before and after its rows.
+constexpr int64_t kSlotBytes = 32 << 10;
 // Inputs above this do not stay in L2 (126 MB, beside what is written).
 constexpr int64_t kOnceBytes = 64 << 20;
 
@@ -218,10 +262,18 @@ Plan plan(NormParams& p, int V, size_t esize) {
   };
   const int sms = device_sm_count();
   // whole groups of at least 32 bytes a row, so that no sector is read twice;
-  // of 64, with half as many blocks, where that still fills the SMs
+  // of 64, with half as many blocks, where that still fills the SMs; and wider
+  // where graphs are short, so that a graph's slab is worth a block's while
   int gps = slab_groups(64);
   if ((int64_t)p.G * ((p.groups + gps - 1) / gps) < sms) gps = slab_groups(32);
-  pl.resident = row * p.N <= kResidentBytes && gps * group * (p.N / p.G) <= kResidentSlabBytes;
+  const int64_t rows = p.N / p.G + 1;
+  if (rows * gps * group < kResidentWorth) {
+    int wide = slab_groups(kResidentWorth / rows);
+    if ((int64_t)wide * p.cg / V > 256) wide = 256 * V / p.cg;  // one tile of vectors
+    if (wide > gps) gps = wide;
+  }
+  pl.resident = row * p.N <= (V > 2 ? kResidentBytes : kResidentNarrowBytes) &&
+                gps * group * (p.N / p.G) <= kResidentSlabBytes;
   pl.nt = kSplitThreads;
   p.gps = gps;
   if (!pl.resident) {
@@ -244,9 +296,11 @@ Plan plan(NormParams& p, int V, size_t esize) {
     }
   }
   pl.slabs = (p.groups + p.gps - 1) / p.gps;
-  // one slot for every block that can be resident, of at least 64 rows
+  // one slot for every block that can be resident, of at least 64 rows and 32 KB
   const int64_t want = (int64_t)sms * split_blocks(pl.nt);
-  const int64_t R = ((int64_t)p.N * pl.slabs + want - 1) / want;
+  const int64_t least = kSlotBytes / ((int64_t)p.gps * group);
+  int64_t R = ((int64_t)p.N * pl.slabs + want - 1) / want;
+  if (R < least) R = least;
   p.R = (int)(R < 64 ? 64 : R);
   p.slots = p.N / p.R + p.G;
   p.once = row * p.N > kOnceBytes;
@@ -260,6 +314,11 @@ cudaError_t with_threads(int nt, F&& f) {
   }
   return f.template operator()<kSplitThreads>();
 }
+
+// Many graphs of a few slots each on average: joining them block by block costs
+// more than the passes (50,000 x 480 bf16 in 2,000 graphs, training: 1,180 us with
+// a block for each join, 340 with a warp or a thread).
+bool few_slots(const NormParams& p) { return p.G > 1 && p.slots / p.G <= 16; }
 
 dim3 split_grid(const NormParams& p, int slabs) {
   const int64_t x = ((int64_t)device_sm_count() * 16 + slabs - 1) / slabs;
@@ -279,7 +338,11 @@ cudaError_t norm_fwd(kmip_dtype_t dtype, int v, int act, NormParams p, cudaStrea
     return with_threads<V>(pl.nt, [&]<int NT>() {
       norm_stats_split<T, V, NT><<<grid, NT, 0, stream>>>(p);
       const int64_t joins = (int64_t)p.G * p.groups;
-      norm_join_stats<<<(unsigned)(joins < 65536 ? joins : 65536), 256, 0, stream>>>(p);
+      if (few_slots(p))
+        norm_join_stats_few<<<(unsigned)(joins < 65536 * 256ll ? (joins + 255) / 256 : 65536),
+                              256, 0, stream>>>(p);
+      else
+        norm_join_stats<<<(unsigned)(joins < 65536 ? joins : 65536), 256, 0, stream>>>(p);
       norm_apply_split<T, V, ACT, NT><<<grid, NT, 0, stream>>>(p);
       return cudaGetLastError();
     });
@@ -314,8 +377,12 @@ cudaError_t norm_bwd(kmip_dtype_t dtype, int v, int act, NormParams p, void* dwe
         p.gchan = gchan;
         const cudaError_t el = with_threads<V>(pl.nt, [&]<int NT>() {
           norm_bwd_sums_split<T, V, ACT, NT><<<grid, NT, sizeof(BwdSmem<NT, V>), stream>>>(p);
-          norm_join_graph<T><<<dim3(tiles, p.G < 65535 ? p.G : 65535), 1024, 0, stream>>>(
-              p, gchan, direct ? dw : nullptr, db);
+          if (few_slots(p))
+            norm_join_graph_few<<<dim3(tiles, p.G < 8 * 65535 ? (p.G + 7) / 8 : 65535), 256, 0,
+                                  stream>>>(p, gchan);
+          else
+            norm_join_graph<T><<<dim3(tiles, p.G < 65535 ? p.G : 65535), 1024, 0, stream>>>(
+                p, gchan, direct ? dw : nullptr, db);
           norm_bwd_apply_split<T, V, ACT, NT><<<grid, NT, 0, stream>>>(p);
           return cudaGetLastError();
         });

@@ -140,7 +140,10 @@ __device__ __forceinline__ int first_slot(const NormParams& p, int g) {
   return (p.offsets ? p.offsets[g] : 0) / p.R + g;
 }
 
-// Graph and rows of a slot; false when the slot holds none.
+// Graph and rows of a slot; false when the slot holds none.  (The same plain
+// search in every thread: everything that follows from it stays in uniform
+// registers.  A search by 32 probes of a warp made the backward's passes over
+// single elements a third slower.)
 __device__ __forceinline__ bool slot_rows(const NormParams& p, int slot, int& g, int& r0,
                                           int& r1) {
   int a = 0, b = p.G - 1;  // last graph whose first slot is <= slot

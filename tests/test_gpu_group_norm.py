@@ -308,3 +308,16 @@ def test_captured_graphs_replay_side_by_side(dev, sizes):
         want = (y, mean, rstd) + binding.group_norm_bwd(dy, x, w, b, mean, rstd, 8, "silu", off)
         for a, c in zip(got, want):
             assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("dtype,N,C,groups,G", [
+    (BF, 60000, 128, 8, 3000),            # resident, short graphs: slabs of a whole row
+    (F32, 30000, 264, 33, 120),           # resident, above 16 MB
+    (BF, 60000, 154, 7, 700),             # split, narrow loads, few slots a graph
+    (F32, 40000, 129, 3, 50)])            # split, 129 channels
+def test_many_graphs(dev, dtype, N, C, groups, G):
+    g = torch.Generator().manual_seed(C)
+    cut = torch.randint(0, N + 1, (G - 1,), generator=g).sort().values.tolist()
+    sizes = [b - a for a, b in zip([0] + cut, cut + [N])]
+    x, w, b, dy, off = _case(sizes, C, dtype, dev, seed=G)
+    _check(x, w, b, dy, off, groups, "silu")
