@@ -19,6 +19,7 @@
 // sizes; launches and the length of the contraction for small ones.
 #include "kmip_act.cuh"
 #include "kmip_ffn.h"
+#include "kmip_launch.cuh"
 
 namespace kmip {
 namespace {
@@ -34,7 +35,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const float* src, bool on) 
                "r"(on ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
 }
@@ -58,7 +61,8 @@ __device__ __forceinline__ void copy_step(uint32_t dst, const float* src, int64_
     const int i = KIN ? id / (kBK / 4) : id % (TM / 4) * 4;
     const int k = KIN ? id % (kBK / 4) * 4 : id / (TM / 4);
     const bool on = i0 + i < extent && k0 + k < K;
-    const float* at = src + (KIN ? (int64_t)(i0 + i) * ld + k0 + k : (int64_t)(k0 + k) * ld + i0 + i);
+    const float* at =
+        src + (KIN ? (int64_t)(i0 + i) * ld + k0 + k : (int64_t)(k0 + k) * ld + i0 + i);
     copy16(dst + (KIN ? i * kPitch + k : k * (TM + 4) + i) * 4, on ? at : src, on);
   }
 }
@@ -114,6 +118,7 @@ constexpr int gemm_smem() { return kStages * 2 * kStepFloats<TM> * 4; }
 
 template <int TM, bool AKIN, bool BKIN>
 __global__ void __launch_bounds__(kThreads, 2) ffn_f32_gemm(const Products ps) {
+  after_previous();
   constexpr int R = TM / 16;  // outputs of a thread per side
   extern __shared__ float4 dyn[];
   float* buffers = reinterpret_cast<float*>(dyn);  // [kStages][A, B]
@@ -192,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 2) ffn_f32_gemm(const Products ps) {
 }
 
 __global__ void __launch_bounds__(kThreads) ffn_f32_join(const Products ps) {
+  after_previous();
   const int64_t total = ps.elems[ps.count];
   for (int64_t i = (blockIdx.x * (int64_t)kThreads + threadIdx.x) * 4; i < total;
        i += (int64_t)gridDim.x * kThreads * 4) {
@@ -215,6 +221,7 @@ template <int ACT, bool BWD, int R, int Q>
 __global__ void __launch_bounds__(kThreads, 2)
 ffn_f32_glu(const float* x, const float* wg, const float* wu, const float* dy, const float* wd,
             int N, int C, int F, float* da, float* db, float* h) {
+  after_previous();
   constexpr int TM = 16 * R, TN = 16 * Q;
   constexpr int kFloatsM = kStepFloats<TM>, kFloatsN = kStepFloats<TN>;
   constexpr int kBuf = kFloatsM + 2 * kFloatsN;  // x, Wg, Wu; or dy, Wd
@@ -405,8 +412,8 @@ cudaError_t launch(const Products& ps, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm_smem<TM>());
   if (e != cudaSuccess) return e;
-  kern<<<dim3(ps.tile0[ps.count], ps.splits), kThreads, gemm_smem<TM>(), stream>>>(ps);
-  return cudaGetLastError();
+  return launch_next(kern, dim3(ps.tile0[ps.count], ps.splits), kThreads, gemm_smem<TM>(), stream,
+                     ps);
 }
 
 template <bool AKIN, bool BKIN>
@@ -419,9 +426,10 @@ cudaError_t run(Products& ps, float* part, cudaStream_t stream) {
   if (ps.splits > 1) {
     const int64_t n4 = (ps.elems[ps.count] + 3) / 4, most = (int64_t)device_sm_count() * 8;
     const int64_t want = (n4 + kThreads - 1) / kThreads;
-    ffn_f32_join<<<(unsigned)(want < most ? want : most), kThreads, 0, stream>>>(ps);
+    return launch_next(ffn_f32_join, dim3((unsigned)(want < most ? want : most)), kThreads, 0,
+                       stream, ps);
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace

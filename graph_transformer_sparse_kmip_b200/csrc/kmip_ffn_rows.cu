@@ -11,6 +11,7 @@
 // order; h stays in fp32 between the two kernels.
 #include "kmip_act.cuh"
 #include "kmip_ffn.h"
+#include "kmip_launch.cuh"
 
 namespace kmip {
 namespace {
@@ -108,6 +109,7 @@ template <typename T, int NR, int CT>
 __global__ void __launch_bounds__(kThreads) ffn_rows_glu(const T* x, const T* wg, const T* wu,
                                                          float* h, int N, int C, int F, int act,
                                                          int S) {
+  after_previous();
   __shared__ float red[kWarps][2 * CT * NR];
   const int warp = threadIdx.x >> 5, group = warp / S, part = warp % S;
   const int f0 = (blockIdx.x * (kWarps / S) + group) * CT, n0 = blockIdx.y * NR;
@@ -138,6 +140,7 @@ __global__ void __launch_bounds__(kThreads) ffn_rows_glu(const T* x, const T* wg
 template <typename T, int NR, int CT>
 __global__ void __launch_bounds__(kThreads) ffn_rows_down(const float* h, const T* wd, T* y, int N,
                                                           int C, int F, int S) {
+  after_previous();
   __shared__ float red[kWarps][CT * NR];
   const int warp = threadIdx.x >> 5, group = warp / S, part = warp % S;
   const int c0 = (blockIdx.x * (kWarps / S) + group) * CT, n0 = blockIdx.y * NR;
@@ -175,9 +178,11 @@ cudaError_t rows_fwd(const FfnArgs& a, float* h, void* y, cudaStream_t stream) {
   ffn_rows_glu<T, NR, CT><<<grid(a.F, sg), kThreads, 0, stream>>>(
       static_cast<const T*>(a.x), static_cast<const T*>(a.wg), static_cast<const T*>(a.wu), h, a.N,
       a.C, a.F, a.act, sg);
-  ffn_rows_down<T, NR, CT><<<grid(a.C, sd), kThreads, 0, stream>>>(
-      h, static_cast<const T*>(a.wd), static_cast<T*>(y), a.N, a.C, a.F, sd);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_next(ffn_rows_down<T, NR, CT>, grid(a.C, sd), kThreads, 0, stream,
+                     (const float*)h, static_cast<const T*>(a.wd), static_cast<T*>(y), a.N, a.C,
+                     a.F, sd);
 }
 
 template <typename T>

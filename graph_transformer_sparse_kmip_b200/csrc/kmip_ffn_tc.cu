@@ -42,6 +42,7 @@
 #include "kmip_ffn.h"
 #include "kmip_gemm.cuh"
 #include "kmip_internal.h"
+#include "kmip_launch.cuh"
 #include "kmip_tensormap.h"
 
 namespace kmip {
@@ -195,6 +196,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  after_previous();
 
   if (warp == kEpiWarps) {
     // ------------------------------------------------------------ producer
@@ -465,6 +467,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
 // was cut, CTA of the pair, 8-column group); 128 threads, one per row.
 template <int BN>
 __global__ void __launch_bounds__(128) ffn_join_kernel(const GemmParams p) {
+  after_previous();
   const int rest = p.tiles - p.whole, tile = p.whole + blockIdx.x, rank = blockIdx.y;
   const int row = threadIdx.x;
   float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -506,11 +509,13 @@ int clusters_for(int64_t tiles) {
 }
 
 template <int MODE, int BN, int ACT>
-cudaError_t launch_gemm(const Maps& maps, const GemmParams& p, int clusters, cudaStream_t stream) {
+cudaError_t launch_gemm(const Maps& maps, const GemmParams& p, int clusters, cudaStream_t stream,
+                        bool next) {
   auto kern = ffn_gemm_kernel<MODE, BN, ACT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        smem_of(MODE));
   if (e != cudaSuccess) return e;
+  if (next) return launch_next(kern, dim3(2 * clusters), kThreads, smem_of(MODE), stream, maps, p);
   kern<<<2 * clusters, kThreads, smem_of(MODE), stream>>>(maps, p);
   return cudaGetLastError();
 }
@@ -519,10 +524,10 @@ template <int MODE>
 cudaError_t launch_act(int act, const Maps& maps, const GemmParams& p, cudaStream_t stream) {
   const int c = clusters_for(p.tiles);
   switch (act) {
-    case KMIP_ACT_SILU: return launch_gemm<MODE, 256, KMIP_ACT_SILU>(maps, p, c, stream);
-    case KMIP_ACT_GELU: return launch_gemm<MODE, 256, KMIP_ACT_GELU>(maps, p, c, stream);
-    case KMIP_ACT_RELU: return launch_gemm<MODE, 256, KMIP_ACT_RELU>(maps, p, c, stream);
-    default: return launch_gemm<MODE, 256, KMIP_ACT_NONE>(maps, p, c, stream);
+    case KMIP_ACT_SILU: return launch_gemm<MODE, 256, KMIP_ACT_SILU>(maps, p, c, stream, false);
+    case KMIP_ACT_GELU: return launch_gemm<MODE, 256, KMIP_ACT_GELU>(maps, p, c, stream, false);
+    case KMIP_ACT_RELU: return launch_gemm<MODE, 256, KMIP_ACT_RELU>(maps, p, c, stream, false);
+    default: return launch_gemm<MODE, 256, KMIP_ACT_NONE>(maps, p, c, stream, false);
   }
 }
 
@@ -577,20 +582,18 @@ size_t part_bytes(const GemmParams& p, int bn) {
   return (size_t)(p.tiles - p.whole) * p.parts * kTileM * bn * sizeof(float);
 }
 
-// The GEMM and, where tiles were cut, the join of their parts.
+// The GEMM (after another kernel of the call) and, where tiles were cut, the
+// join of their parts.
 template <int MODE>
 cudaError_t launch_split(const Maps& m, const GemmParams& p, int bn, cudaStream_t stream) {
   const int rest = p.tiles - p.whole;
   const int c = clusters_for(p.whole + (int64_t)rest * p.parts);
-  const cudaError_t e = bn == 256 ? launch_gemm<MODE, 256, 0>(m, p, c, stream)
-                                  : launch_gemm<MODE, 128, 0>(m, p, c, stream);
+  const cudaError_t e = bn == 256 ? launch_gemm<MODE, 256, 0>(m, p, c, stream, true)
+                                  : launch_gemm<MODE, 128, 0>(m, p, c, stream, true);
   if (e != cudaSuccess || !rest) return e;
   const dim3 grid(rest, 2, bn / 8);
-  if (bn == 256)
-    ffn_join_kernel<256><<<grid, 128, 0, stream>>>(p);
-  else
-    ffn_join_kernel<128><<<grid, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_next(bn == 256 ? ffn_join_kernel<256> : ffn_join_kernel<128>, grid, 128, 0, stream,
+                     p);
 }
 
 GemmParams down_params(const FfnArgs& a, int bn) {

@@ -1,6 +1,7 @@
 // kmip_norm.cu -- group norm per graph with an activation: entry points
 // (kmip_group_norm_fwd, kmip_group_norm_bwd), the choice between the two ways
 // over the graphs, and the kernels of the split one.
+#include "kmip_launch.cuh"
 #include "kmip_norm.cuh"
 
 namespace kmip {
@@ -14,6 +15,7 @@ constexpr int split_blocks(int nt) { return nt == kSplitThreads ? 4 : 2; }
 
 template <typename T, int V, int NT>
 __global__ void __launch_bounds__(NT, split_blocks(NT)) norm_stats_split(const NormParams p) {
+  after_previous();
   __shared__ StatSmem<NT> sm;
   const Slab s = make_slab<NT, V>(p, blockIdx.y);
   for (int slot = blockIdx.x; slot < p.slots; slot += gridDim.x) {
@@ -29,6 +31,7 @@ __global__ void __launch_bounds__(NT, split_blocks(NT)) norm_stats_split(const N
 
 // One block per (graph, group): joins the graph's slots in a fixed order.
 __global__ void __launch_bounds__(256) norm_join_stats(const NormParams p) {
+  after_previous();
   __shared__ double s0[8], s1[8];
   for (int64_t i = blockIdx.x; i < (int64_t)p.G * p.groups; i += gridDim.x) {
     const int g = (int)(i / p.groups), j = (int)(i % p.groups);
@@ -68,6 +71,7 @@ __global__ void __launch_bounds__(256) norm_join_stats(const NormParams p) {
 
 // The same for graphs of a few slots: one thread per (graph, group).
 __global__ void __launch_bounds__(256) norm_join_stats_few(const NormParams p) {
+  after_previous();
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < (int64_t)p.G * p.groups;
        i += gridDim.x * 256ll) {
     const int g = (int)(i / p.groups), j = (int)(i % p.groups);
@@ -87,6 +91,7 @@ __global__ void __launch_bounds__(256) norm_join_stats_few(const NormParams p) {
 
 template <typename T, int V, int ACT, int NT>
 __global__ void __launch_bounds__(NT, split_blocks(NT)) norm_apply_split(const NormParams p) {
+  after_previous();
   __shared__ float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
   const Slab s = make_slab<NT, V>(p, blockIdx.y);
   for (int slot = p.slots - 1 - (int)blockIdx.x; slot >= 0; slot -= gridDim.x) {
@@ -102,6 +107,7 @@ __global__ void __launch_bounds__(NT, split_blocks(NT)) norm_apply_split(const N
 template <typename T, int V, int ACT, int NT>
 __global__ void __launch_bounds__(NT, NT == kSplitThreads ? 3 : 2)
 norm_bwd_sums_split(const NormParams p) {
+  after_previous();
   extern __shared__ float4 dyn[];
   BwdSmem<NT, V>& sm = *reinterpret_cast<BwdSmem<NT, V>*>(dyn);
   __shared__ float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
@@ -111,8 +117,8 @@ norm_bwd_sums_split(const NormParams p) {
     if (!slot_rows(p, slot, g, r0, r1)) continue;
     load_stats(p, s, g, mean, rstd);
     __syncthreads();
-    slab_bwd_sums<T, V, ACT, NT, false, kRowsTwo<V>>(p, s, r0, r1, mean, rstd, p.chan + (int64_t)slot * 2 * p.C,
-                                   true, sm);
+    slab_bwd_sums<T, V, ACT, NT, false, kRowsTwo<V>>(
+        p, s, r0, r1, mean, rstd, p.chan + (int64_t)slot * 2 * p.C, true, sm);
   }
 }
 
@@ -138,6 +144,7 @@ __device__ __forceinline__ float join_column(const float* src, int64_t cols, int
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_join_graph(const NormParams p, float* gchan, T* dw,
                                                         T* db) {
+  after_previous();
   __shared__ float red[32][33];
   const int64_t cols = 2 * (int64_t)p.C, c0 = blockIdx.x * 32ll;
   for (int g = blockIdx.y; g < p.G; g += gridDim.y) {
@@ -159,6 +166,7 @@ __global__ void __launch_bounds__(1024) norm_join_graph(const NormParams p, floa
 
 // The same for graphs of a few slots: one warp per graph and 32 columns.
 __global__ void __launch_bounds__(256) norm_join_graph_few(const NormParams p, float* gchan) {
+  after_previous();
   const int64_t cols = 2 * (int64_t)p.C, col = blockIdx.x * 32ll + (threadIdx.x & 31);
   if (col >= cols) return;
   for (int64_t g = blockIdx.y * 8ll + (threadIdx.x >> 5); g < p.G; g += gridDim.y * 8ll) {
@@ -176,6 +184,7 @@ __global__ void __launch_bounds__(256) norm_join_graph_few(const NormParams p, f
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_join_params(const float* src, int rows, int C, T* dw,
                                                          T* db) {
+  after_previous();
   __shared__ float red[32][33];
   const int64_t cols = 2 * (int64_t)C, c0 = blockIdx.x * 32ll;
   const float sum = join_column(src, cols, rows, c0 + (threadIdx.x & 31), red);
@@ -189,6 +198,7 @@ __global__ void __launch_bounds__(1024) norm_join_params(const float* src, int r
 template <typename T, int V, int ACT, int NT>
 __global__ void __launch_bounds__(NT, NT == kSplitThreads ? 3 : 2)
 norm_bwd_apply_split(const NormParams p) {
+  after_previous();
   __shared__ float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
   __shared__ float m1[kMaxSlabGroups], m2[kMaxSlabGroups];
   const Slab s = make_slab<NT, V>(p, blockIdx.y);
@@ -339,11 +349,13 @@ cudaError_t norm_fwd(kmip_dtype_t dtype, int v, int act, NormParams p, cudaStrea
       norm_stats_split<T, V, NT><<<grid, NT, 0, stream>>>(p);
       const int64_t joins = (int64_t)p.G * p.groups;
       if (few_slots(p))
-        norm_join_stats_few<<<(unsigned)(joins < 65536 * 256ll ? (joins + 255) / 256 : 65536),
-                              256, 0, stream>>>(p);
+        launch_next(norm_join_stats_few,
+                    dim3(joins < 65536 * 256ll ? (unsigned)((joins + 255) / 256) : 65536u), 256, 0,
+                    stream, p);
       else
-        norm_join_stats<<<(unsigned)(joins < 65536 ? joins : 65536), 256, 0, stream>>>(p);
-      norm_apply_split<T, V, ACT, NT><<<grid, NT, 0, stream>>>(p);
+        launch_next(norm_join_stats, dim3(joins < 65536 ? (unsigned)joins : 65536u), 256, 0,
+                    stream, p);
+      launch_next(norm_apply_split<T, V, ACT, NT>, grid, NT, 0, stream, p);
       return cudaGetLastError();
     });
   });
@@ -378,12 +390,12 @@ cudaError_t norm_bwd(kmip_dtype_t dtype, int v, int act, NormParams p, void* dwe
         const cudaError_t el = with_threads<V>(pl.nt, [&]<int NT>() {
           norm_bwd_sums_split<T, V, ACT, NT><<<grid, NT, sizeof(BwdSmem<NT, V>), stream>>>(p);
           if (few_slots(p))
-            norm_join_graph_few<<<dim3(tiles, p.G < 8 * 65535 ? (p.G + 7) / 8 : 65535), 256, 0,
-                                  stream>>>(p, gchan);
+            launch_next(norm_join_graph_few, dim3(tiles, p.G < 8 * 65535 ? (p.G + 7) / 8 : 65535),
+                        256, 0, stream, p, gchan);
           else
-            norm_join_graph<T><<<dim3(tiles, p.G < 65535 ? p.G : 65535), 1024, 0, stream>>>(
-                p, gchan, direct ? dw : nullptr, db);
-          norm_bwd_apply_split<T, V, ACT, NT><<<grid, NT, 0, stream>>>(p);
+            launch_next(norm_join_graph<T>, dim3(tiles, p.G < 65535 ? p.G : 65535), 1024, 0,
+                        stream, p, gchan, direct ? dw : nullptr, db);
+          launch_next(norm_bwd_apply_split<T, V, ACT, NT>, grid, NT, 0, stream, p);
           return cudaGetLastError();
         });
         if (el != cudaSuccess) return el;
@@ -391,7 +403,8 @@ cudaError_t norm_bwd(kmip_dtype_t dtype, int v, int act, NormParams p, void* dwe
         nsums = p.G;
         params = params && !direct;
       }
-      if (params) norm_join_params<T><<<tiles, 1024, 0, stream>>>(sums, nsums, p.C, dw, db);
+      if (params)
+        launch_next(norm_join_params<T>, dim3(tiles), 1024, 0, stream, sums, nsums, p.C, dw, db);
       return cudaGetLastError();
     });
   const cudaError_t ef = cudaFreeAsync(scratch, stream);
@@ -404,7 +417,8 @@ int vector_width(const NormParams& p, size_t esize, bool bwd) {
   for (int v : options) {
     const uint64_t bytes = v * esize;
     auto off = [&](const void* q) { return reinterpret_cast<uintptr_t>(q) % bytes != 0; };
-    if (p.cg % v || off(p.x) || off(p.w) || off(p.b) || (bwd ? off(p.dy) || off(p.dx) : off(p.y))) continue;
+    if (p.cg % v || off(p.x) || off(p.w) || off(p.b)) continue;
+    if (bwd ? off(p.dy) || off(p.dx) : off(p.y)) continue;
     return v;
   }
   return 1;

@@ -77,7 +77,8 @@ struct Row {
     if constexpr (sizeof(T) == 4) {
       const float* q = reinterpret_cast<const float*>(&raw);
 #pragma unroll
-      for (int e = 0; e < P; ++e) f[e] = make_float2(q[V > 1 ? 2 * e : 0], V > 1 ? q[2 * e + 1] : 0.f);
+      for (int e = 0; e < P; ++e)
+        f[e] = make_float2(q[V > 1 ? 2 * e : 0], V > 1 ? q[2 * e + 1] : 0.f);
     } else if constexpr (V == 1) {
       f[0] = make_float2(__uint_as_float((uint32_t)raw << 16), 0.f);
     } else {

@@ -4,6 +4,7 @@
 // Two shapes of block: 256 threads that hold up to eight rows each, and, when
 // there are fewer blocks than SMs, 1,024 threads that hold up to two (one
 // graph of 1,024 x 32 fp32: a quarter of the steps in a row).
+#include "kmip_launch.cuh"
 #include "kmip_norm.cuh"
 
 namespace kmip {
@@ -55,6 +56,7 @@ __device__ __forceinline__ float group_sum(const NormParams& p, const Slab& s, f
 
 template <typename T, int V, int ACT, int NT, int HOLD>
 __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_fwd_resident(const NormParams p) {
+  after_previous();
   __shared__ StatSmem<NT> sm;
   const Slab s = make_slab<NT, V>(p, blockIdx.y);
   for (int g = blockIdx.x; g < p.G; g += gridDim.x) {
@@ -119,6 +121,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_fwd_resident(const
 
 template <typename T, int V, int ACT, int NT, int HOLD>
 __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_bwd_resident(const NormParams p) {
+  after_previous();
   extern __shared__ float4 dyn[];
   BwdSmem<NT, V>& sm = *reinterpret_cast<BwdSmem<NT, V>*>(dyn);
   __shared__ float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
