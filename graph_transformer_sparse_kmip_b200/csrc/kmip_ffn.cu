@@ -9,7 +9,7 @@ kmip_status_t check_ffn(int64_t N, int C, int F, int act, int dtype) {
   if (N < 0 || N > INT32_MAX || C < 1 || F < 1) return KMIP_ERR_INVALID_ARG;
   if (dtype != KMIP_BF16 && dtype != KMIP_F32) return KMIP_ERR_INVALID_ARG;
   if (act < KMIP_ACT_NONE || act > KMIP_ACT_RELU) return KMIP_ERR_INVALID_ARG;
-  if (C % 8 || F % 8 || C > 65536 || F > 65536) return KMIP_ERR_UNSUPPORTED;
+  if (N > kMaxRows || C % 8 || F % 8 || C > 65536 || F > 65536) return KMIP_ERR_UNSUPPORTED;
   // tiles are counted in 32 bits
   const int64_t wide = C > F ? C : F;
   if ((N / 64 + 1) * (wide / 64 + 1) * 3 > INT32_MAX) return KMIP_ERR_UNSUPPORTED;

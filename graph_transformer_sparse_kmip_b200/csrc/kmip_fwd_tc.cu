@@ -55,10 +55,10 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <mutex>
 
 #include "kmip_internal.h"
 #include "kmip_sm100.cuh"
-#include "kmip_tensormap.h"
 
 namespace kmip {
 namespace {
@@ -813,11 +813,41 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 
 // ------------------------------------------------------------------ host side
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static std::once_flag once;
+  static EncodeTiledFn fn = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
 // [N rows, H*d columns] bf16, box = (region width, 128 rows), swizzled.
 template <int D>
 bool make_map(CUtensorMap* m, const void* ptr, int N, int H) {
   using C = Cfg<D, kRegK>;
-  return encode_map_2d(m, ptr, (uint64_t)N, (uint64_t)H * D, C::kRegionElems, 128u);
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)H * D, (cuuint64_t)N};
+  const cuuint64_t strides[1] = {(cuuint64_t)H * D * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)C::kRegionElems, 128u};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapSwizzle sw = C::kRowBytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                : C::kRowBytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                     : CU_TENSOR_MAP_SWIZZLE_128B;
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, int KCAP, bool DIAG>

@@ -96,6 +96,10 @@ cudaError_t launch_gather(kmip_dtype_t dtype, const GatherArgs& a, cudaStream_t 
 // its scratch from the library's pool (scratch_alloc).
 cudaError_t launch_bwd_deterministic(kmip_dtype_t dtype, const BwdArgs& a, cudaStream_t stream);
 
+// Most rows of the norm and the feed-forward block: row numbers of a block's
+// next steps, past the last row, stay within an int.
+constexpr int64_t kMaxRows = INT32_MAX - (1 << 20);
+
 int device_sm_count();
 
 // Stream-ordered allocation from the library's own memory pool on the

@@ -430,7 +430,8 @@ kmip_status_t check_norm(const int32_t* offsets, int64_t N, int C, int groups, i
   if (dtype != KMIP_BF16 && dtype != KMIP_F32) return KMIP_ERR_INVALID_ARG;
   if (act < KMIP_ACT_NONE || act > KMIP_ACT_RELU) return KMIP_ERR_INVALID_ARG;
   if (offsets && num_graphs < 1) return KMIP_ERR_INVALID_ARG;
-  if (C > 65536 || N * (int64_t)C > ((int64_t)1 << 40)) return KMIP_ERR_UNSUPPORTED;
+  if (N > kMaxRows || C > 65536 || N * (int64_t)C > ((int64_t)1 << 40))
+    return KMIP_ERR_UNSUPPORTED;
   // slots are numbered in 32 bits
   if (offsets && N / 64 + (int64_t)num_graphs > INT32_MAX) return KMIP_ERR_UNSUPPORTED;
   return KMIP_OK;

@@ -319,7 +319,8 @@ kmip_status_t kmip_rotary(const void* x, int64_t x_row, int64_t x_head, const vo
  *              1 / sqrt(eps)); the backward takes them.
  * Statistics are held in fp32 (per thread, by batches with their own mean)
  * and joined in fp64; results do not change from run to run.
- * Supported: 1 <= groups <= C <= 65536, groups divides C; eps > 0.  x, y and
+ * Supported: N <= 2^31 - 2^20 - 1; 1 <= groups <= C <= 65536, groups divides C;
+ * eps > 0.  x, y and
  * the parameters need only their element's alignment; 16-byte aligned rows
  * with C / groups a multiple of 8 (bf16) or 4 (fp32) are the fast case.
  */
@@ -355,8 +356,8 @@ kmip_status_t kmip_group_norm_bwd(const void* dy, const void* x, const void* wei
  * up to 16 rows of either type, run on fp32 fused multiply-adds (few rows are
  * bound by reading the weights).  Takes N F elements of scratch (up to 16
  * rows: fp32 ones).
- * Supported: C and F multiples of 8, 8 .. 65536; all pointers 16-byte
- * aligned; y may not overlap an input.
+ * Supported: N <= 2^31 - 2^20 - 1; C and F multiples of 8, 8 .. 65536; all
+ * pointers 16-byte aligned; y may not overlap an input.
  */
 kmip_status_t kmip_ffn_fwd(const void* x, const void* Wg, const void* Wu, const void* Wd,
                            int64_t N, int C, int F, kmip_act_t act, void* y,

@@ -64,7 +64,7 @@ def test_group_norm_refusals(lib):
         assert _norm_fwd(lib, **kw) == INVALID, kw
     for kw in both + (dict(dy=None), dict(dx=None), dict(dw=None), dict(db=None), dict(dx=A)):
         assert _norm_bwd(lib, **kw) == INVALID, kw
-    for kw in (dict(C=65537, groups=1), dict(N=(1 << 31) - 1, C=1024)):
+    for kw in (dict(C=65537, groups=1), dict(N=(1 << 31) - 1), dict(N=1 << 30, C=2048)):
         assert _norm_fwd(lib, **kw) == UNSUP and _norm_bwd(lib, **kw) == UNSUP, kw
 
 
@@ -86,8 +86,8 @@ def test_ffn_refusals(lib):
     for kw in both + (dict(dy=None), dict(dx=None), dict(dwg=None), dict(dwu=None),
                       dict(dwd=None), dict(dx=A + 8), dict(dwd=A + 8)):
         assert _ffn_bwd(lib, **kw) == INVALID, kw
-    for kw in (dict(C=36), dict(F=60), dict(C=65544), dict(F=65544),
-               dict(N=(1 << 31) - 1, F=65536)):
+    for kw in (dict(C=36), dict(F=60), dict(C=65544), dict(F=65544), dict(N=(1 << 31) - 1),
+               dict(N=1 << 30, F=65536)):
         assert _ffn_fwd(lib, **kw) == UNSUP and _ffn_bwd(lib, **kw) == UNSUP, kw
     assert _ffn_fwd(lib, N=0, x=None, y=None) == 0
 
