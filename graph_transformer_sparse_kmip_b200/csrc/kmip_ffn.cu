@@ -27,6 +27,23 @@ bool all_aligned(P... ptrs) {
   return (... && (ptrs && aligned16(ptrs)));
 }
 
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+// Whether two of the spans share bytes, one of them among the first `outs`.
+template <size_t N>
+bool overlapping(const Span (&s)[N], size_t outs) {
+  for (size_t i = 0; i < outs; ++i)
+    for (size_t j = i + 1; j < N; ++j) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p);
+      const uintptr_t b = reinterpret_cast<uintptr_t>(s[j].p);
+      if (a < b + s[j].bytes && b < a + s[i].bytes) return true;
+    }
+  return false;
+}
+
 size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 }  // namespace
@@ -41,6 +58,9 @@ extern "C" __attribute__((visibility("default"))) kmip_status_t kmip_ffn_fwd(
   if (st != KMIP_OK) return st;
   if (N == 0) return KMIP_OK;
   if (!all_aligned(x, Wg, Wu, Wd, y)) return KMIP_ERR_INVALID_ARG;
+  const size_t es = dtype == KMIP_BF16 ? 2 : 4, nc = es * N * C, cf = es * C * F;
+  if (overlapping({{y, nc}, {x, nc}, {Wg, cf}, {Wu, cf}, {Wd, cf}}, 1))
+    return KMIP_ERR_INVALID_ARG;
   int* status = status_ptr();
   if (!status) return KMIP_ERR_CUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
@@ -77,13 +97,17 @@ extern "C" __attribute__((visibility("default"))) kmip_status_t kmip_ffn_bwd(
   if (st != KMIP_OK) return st;
   if (!all_aligned(Wg, Wu, Wd, dWg, dWu, dWd)) return KMIP_ERR_INVALID_ARG;
   if (N > 0 && !all_aligned(dy, x, dx)) return KMIP_ERR_INVALID_ARG;
+  const size_t es = dtype == KMIP_BF16 ? 2 : 4, nf = (size_t)N * F;
+  const size_t nc = es * N * C, cf = es * C * F;
+  if (overlapping({{dx, nc}, {dWg, cf}, {dWu, cf}, {dWd, cf}, {dy, nc}, {x, nc}, {Wg, cf},
+                   {Wu, cf}, {Wd, cf}}, 4))
+    return KMIP_ERR_INVALID_ARG;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const size_t es = dtype == KMIP_BF16 ? 2 : 4, nf = (size_t)N * F, cf = (size_t)C * F;
   cudaError_t e;
   if (N == 0) {
-    e = cudaMemsetAsync(dWg, 0, cf * es, stream);
-    if (e == cudaSuccess) e = cudaMemsetAsync(dWu, 0, cf * es, stream);
-    if (e == cudaSuccess) e = cudaMemsetAsync(dWd, 0, cf * es, stream);
+    e = cudaMemsetAsync(dWg, 0, cf, stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dWu, 0, cf, stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dWd, 0, cf, stream);
     return to_status(e);
   }
   int* status = status_ptr();

@@ -357,7 +357,7 @@ kmip_status_t kmip_group_norm_bwd(const void* dy, const void* x, const void* wei
  * bound by reading the weights).  Takes N F elements of scratch (up to 16
  * rows: fp32 ones).
  * Supported: N <= 2^31 - 2^20 - 1; C and F multiples of 8, 8 .. 65536; all
- * pointers 16-byte aligned; y may not overlap an input.
+ * pointers 16-byte aligned; y may not overlap an input (KMIP_ERR_INVALID_ARG).
  */
 kmip_status_t kmip_ffn_fwd(const void* x, const void* Wg, const void* Wu, const void* Wd,
                            int64_t N, int C, int F, kmip_act_t act, void* y,
@@ -371,7 +371,8 @@ kmip_status_t kmip_ffn_fwd(const void* x, const void* Wg, const void* Wu, const 
  * the gradients is that of the projections' gradients and h.  Takes 3 N F
  * elements of scratch and at most 78 MB of partial sums, which are joined in
  * a fixed order: results do not change from run to run.  N = 0 gives zero
- * weight gradients.  Outputs may not overlap inputs or one another.
+ * weight gradients.  Outputs may not overlap inputs or one another
+ * (KMIP_ERR_INVALID_ARG).
  */
 kmip_status_t kmip_ffn_bwd(const void* dy, const void* x, const void* Wg, const void* Wu,
                            const void* Wd, int64_t N, int C, int F, kmip_act_t act, void* dx,
