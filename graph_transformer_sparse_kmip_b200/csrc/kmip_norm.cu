@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256) norm_join_stats_few(const NormParams p) {
        i += gridDim.x * 256ll) {
     const int g = (int)(i / p.groups), j = (int)(i % p.groups);
     int lo, hi;
-    if (!graph_rows(p, g, lo, hi)) continue;
+    if (!graph_rows(p, g, lo, hi, true)) continue;
     const int a = first_slot(p, g), n = (int)(((int64_t)hi - lo + p.R - 1) / p.R);
     double x = 0.0, q = 0.0;
 #pragma unroll 4
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(256) norm_join_graph_few(const NormParams p, f
   if (col >= cols) return;
   for (int64_t g = blockIdx.y * 8ll + (threadIdx.x >> 5); g < p.G; g += gridDim.y * 8ll) {
     int lo, hi;
-    if (!graph_rows(p, (int)g, lo, hi)) lo = hi = 0;
+    if (!graph_rows(p, (int)g, lo, hi, (threadIdx.x & 31) == 0)) lo = hi = 0;
     const int n = (int)(((int64_t)hi - lo + p.R - 1) / p.R);
     const float* src = p.chan + (hi > lo ? (int64_t)first_slot(p, (int)g) * cols : 0) + col;
     float a = 0.f;
@@ -432,8 +432,8 @@ kmip_status_t check_norm(const int32_t* offsets, int64_t N, int C, int groups, i
   if (offsets && num_graphs < 1) return KMIP_ERR_INVALID_ARG;
   if (N > kMaxRows || C > 65536 || N * (int64_t)C > ((int64_t)1 << 40))
     return KMIP_ERR_UNSUPPORTED;
-  // slots are numbered in 32 bits
-  if (offsets && N / 64 + (int64_t)num_graphs > INT32_MAX) return KMIP_ERR_UNSUPPORTED;
+  // graphs and slots are numbered, and stepped over, in 32 bits
+  if (offsets && N / 64 + (int64_t)num_graphs > kMaxRows) return KMIP_ERR_UNSUPPORTED;
   return KMIP_OK;
 }
 

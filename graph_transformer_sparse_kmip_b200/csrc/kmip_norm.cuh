@@ -126,13 +126,19 @@ __device__ __forceinline__ float2 vfma(float2 a, float2 b, float2 c) {
 
 // ---------------------------------------------------------------- row ranges
 // Node range of graph g; false (and a status) when its offsets are malformed.
-__device__ __forceinline__ bool graph_rows(const NormParams& p, int g, int& lo, int& hi) {
+// One of the threads that ask for the same graph reports.
+__device__ __forceinline__ bool graph_rows(const NormParams& p, int g, int& lo, int& hi,
+                                           bool reports) {
   lo = p.offsets ? p.offsets[g] : 0;
   hi = p.offsets ? p.offsets[g + 1] : p.N;
   const bool ok = lo >= 0 && lo <= hi && hi <= p.N && (g > 0 || lo == 0) &&
                   (g < p.G - 1 || hi == p.N);
-  if (!ok && threadIdx.x == 0) record_status(p.status, KMIP_ERR_BAD_OFFSETS);
+  if (!ok && reports) record_status(p.status, KMIP_ERR_BAD_OFFSETS);
   return ok;
+}
+// (the whole block asks)
+__device__ __forceinline__ bool graph_rows(const NormParams& p, int g, int& lo, int& hi) {
+  return graph_rows(p, g, lo, hi, threadIdx.x == 0);
 }
 
 // Slots: graph g owns slots [lo / R + g, ...), one per R rows; no two graphs'
@@ -149,7 +155,7 @@ __device__ __forceinline__ bool slot_rows(const NormParams& p, int slot, int& g,
                                           int& r1) {
   int a = 0, b = p.G - 1;  // last graph whose first slot is <= slot
   while (a < b) {
-    const int m = (a + b + 1) >> 1;
+    const int m = a + ((b - a + 1) >> 1);
     if (first_slot(p, m) <= slot) a = m; else b = m - 1;
   }
   g = a;
@@ -433,7 +439,7 @@ __device__ void slab_apply(const NormParams& p, const Slab& s, int r0, int r1, c
 }
 
 // ---------------------------------------------------------------- backward
-// (Dynamic shared memory: at most 42 KB.)
+// (Dynamic shared memory: at most 42 KB with 256 threads, 162 KB with 1,024.)
 template <int NT, int V>
 struct BwdSmem {
   float red[2][NT * V / 2 * 3];  // [channel of the tile][TY, or TY + 1 if even]

@@ -93,6 +93,8 @@ class AxisRotary(torch.nn.Module):
     def __init__(self, d: int, axes: int, base: float = 10000.0, sections=None,
                  pairs: int | None = None, interleaved: bool = False):
         super().__init__()
+        if axes < 1:
+            raise ValueError("axes must be positive")
         if sections is None:
             pairs = d // 2 if pairs is None else pairs
             sections = [pairs // axes + (a < pairs % axes) for a in range(axes)]
@@ -110,8 +112,11 @@ class AxisRotary(torch.nn.Module):
         """(freq, axis) on `device`."""
         device = torch.device(device)
         if device not in self._tables:
-            self._tables[device] = (torch.tensor(self._freq, dtype=torch.float64, device=device),
-                                    torch.tensor(self._axis, dtype=torch.int32, device=device))
+            # not inference tensors, even when first made there: training saves them
+            with torch.inference_mode(False):
+                self._tables[device] = (
+                    torch.tensor(self._freq, dtype=torch.float64, device=device),
+                    torch.tensor(self._axis, dtype=torch.int32, device=device))
         return self._tables[device]
 
     def forward(self, x, pos):
@@ -150,7 +155,7 @@ class GraphGroupNorm(torch.nn.Module):
     def __init__(self, channels: int, groups: int, eps: float = 1e-5, act: str = "none",
                  affine: bool = True, dtype=torch.bfloat16, device=None):
         super().__init__()
-        if channels % groups:
+        if groups < 1 or channels % groups:
             raise ValueError("channels must be a multiple of groups")
         binding._act_code(act)
         self.groups, self.eps, self.act = groups, eps, act

@@ -271,6 +271,27 @@ def test_malformed_offsets_of_large_graphs_are_reported(dev):
         assert e.value.code == 4
 
 
+@pytest.mark.parametrize("at", [1, 1001, 1999])
+def test_malformed_offsets_of_many_graphs_are_reported(dev, at):
+    """Wherever among many graphs they are, and only there: 2,000 graphs of 30
+    nodes with 155 channels, too many bytes for one block a graph."""
+    x, w, b, dy, off = _case([30] * 2000, 155, BF, dev)
+    mean = torch.zeros((2000, 31), device=dev)
+    off[at] += 31  # behind the graph's own end
+    binding.group_norm_fwd(x, w, b, 31, 1e-5, "silu", off)
+    with pytest.raises(KmipError) as e:
+        binding.check_status()
+    assert e.value.code == 4
+    binding.group_norm_bwd(dy, x, w, b, mean, mean + 1, 31, "silu", off)
+    with pytest.raises(KmipError) as e:
+        binding.check_status()
+    assert e.value.code == 4
+    off[at] -= 31
+    y, mean, rstd = binding.group_norm_fwd(x, w, b, 31, 1e-5, "silu", off)
+    binding.group_norm_bwd(dy, x, w, b, mean, rstd, 31, "silu", off)
+    binding.check_status()
+
+
 def test_no_nodes(dev):
     x = torch.empty((0, 64), device=dev)
     w, b = torch.ones(64, device=dev), torch.zeros(64, device=dev)

@@ -64,7 +64,8 @@ def test_group_norm_refusals(lib):
         assert _norm_fwd(lib, **kw) == INVALID, kw
     for kw in both + (dict(dy=None), dict(dx=None), dict(dw=None), dict(db=None), dict(dx=A)):
         assert _norm_bwd(lib, **kw) == INVALID, kw
-    for kw in (dict(C=65537, groups=1), dict(N=(1 << 31) - 1), dict(N=1 << 30, C=2048)):
+    for kw in (dict(C=65537, groups=1), dict(N=(1 << 31) - 1), dict(N=1 << 30, C=2048),
+               dict(off=A, G=(1 << 31) - 1), dict(off=A, N=1 << 28, G=(1 << 31) - (1 << 22))):
         assert _norm_fwd(lib, **kw) == UNSUP and _norm_bwd(lib, **kw) == UNSUP, kw
 
 
@@ -90,6 +91,18 @@ def test_ffn_refusals(lib):
                dict(N=1 << 30, F=65536)):
         assert _ffn_fwd(lib, **kw) == UNSUP and _ffn_bwd(lib, **kw) == UNSUP, kw
     assert _ffn_fwd(lib, N=0, x=None, y=None) == 0
+
+
+def test_ffn_refuses_outputs_that_overlap(lib):
+    # x, y and their gradients take 512 bytes here, a weight 4,096
+    B = 6 * A
+    for kw in (dict(y=A), dict(x=B, y=B + 496), dict(x=B, y=B - 496), dict(wg=B, y=B + 4080),
+               dict(wu=B, y=B - 496), dict(wd=B, y=B + 16)):
+        assert _ffn_fwd(lib, **kw) == INVALID, kw
+    for kw in (dict(dx=A), dict(x=B, dx=B + 496), dict(dy=B, dx=B - 496), dict(wd=B, dx=B + 4080),
+               dict(dwg=A), dict(dwu=3 * A), dict(dwd=4 * A + 4080), dict(dwg=2 * A + 496),
+               dict(wu=B, dwu=B), dict(dy=B, dwd=B - 4080)):
+        assert _ffn_bwd(lib, **kw) == INVALID, kw
 
 
 def test_binding_refuses_what_it_cannot_pass():
@@ -120,3 +133,26 @@ def test_binding_refuses_what_it_cannot_pass():
         binding.ffn_fwd(y, g, g, d)
     with pytest.raises(ValueError, match="expected"):
         binding.ffn_fwd(y, g[0], g, d)
+
+
+def test_rotary_tables_made_in_inference_mode_can_train():
+    """A layer that answers first and trains later keeps its tables."""
+    from graph_transformer_sparse_kmip_b200.layer import AxisRotary
+    r = AxisRotary(32, 2)
+    with torch.inference_mode():
+        freq, axis = r.tables("cpu")
+    assert not freq.is_inference() and not axis.is_inference()
+    w = torch.ones(16, dtype=torch.float64, requires_grad=True)
+    (w * freq).sum().backward()
+    assert torch.equal(w.grad, freq)
+
+
+def test_module_refusals():
+    from graph_transformer_sparse_kmip_b200.layer import AxisRotary, GraphGroupNorm
+    for kw in (dict(axes=0), dict(axes=-1), dict(axes=2, sections=[8]), dict(axes=1, pairs=17),
+               dict(axes=2, sections=[-1, 4])):
+        with pytest.raises(ValueError):
+            AxisRotary(32, **kw)
+    for channels, groups in ((32, 0), (32, 5), (32, -4)):
+        with pytest.raises(ValueError):
+            GraphGroupNorm(channels, groups)
