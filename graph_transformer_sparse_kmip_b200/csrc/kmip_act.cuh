@@ -123,17 +123,22 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 
 // Sigmoids of two values, z limited from below to kLeast first (silu(kLeast) is
-// -5e-18; a NaN stays).  bf16: both quotients out of one reciprocal, of the
-// product of the denominators, which that limit keeps under 2^127: three
-// slow-pipe instructions for two values instead of four.
+// -3e-18).  bf16: both quotients out of one reciprocal, of the product of the
+// denominators, which that limit keeps under 2^127: three slow-pipe
+// instructions for two values instead of four.  A NaN stays in z and so in what
+// the sigmoid is multiplied with, but is not let into that product, where the
+// other value would meet it.
 constexpr float kLeast = -44.f;
 template <typename T>
 __device__ __forceinline__ float2 sigmoid2(float2& z) {
   if constexpr (sizeof(T) == 2) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float2 t = mul2(z, splat2(-kLog2e));  // (fminf drops a NaN)
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(z.x) : "f"(kLeast));
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(z.y) : "f"(kLeast));
-    const float2 t = mul2(z, splat2(-1.4426950408889634f));
-    const float2 q = add2(make_float2(ex2_fast(t.x), ex2_fast(t.y)), splat2(1.f));
+    const float2 q = add2(make_float2(ex2_fast(fminf(t.x, -kLog2e * kLeast)),
+                                      ex2_fast(fminf(t.y, -kLog2e * kLeast))),
+                          splat2(1.f));
     const float r = rcp_fast(q.x * q.y);
     return make_float2(q.y * r, q.x * r);
   } else {

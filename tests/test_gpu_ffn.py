@@ -138,6 +138,24 @@ def test_rows_do_not_meet(dev, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+def test_a_gate_without_a_number_stays_alone(dev, dtype, act):
+    """Rows of Wg that hold a NaN spoil y and dx, and of the weights' gradients
+    their own rows only."""
+    x, wg, wu, wd, dy = _case(300, 64, 136, dtype, dev)
+    before = binding.ffn_bwd(dy, x, wg, wu, wd, act)
+    bad = [6, 33, 135]
+    rest = [f for f in range(136) if f not in bad]
+    wg[bad, 3] = float("nan")
+    dx, dwg, dwu, dwd = binding.ffn_bwd(dy, x, wg, wu, wd, act)
+    assert torch.equal(dwg[rest], before[1][rest]) and torch.equal(dwu[rest], before[2][rest])
+    assert torch.equal(dwd[:, rest], before[3][:, rest])
+    assert dwu[bad].isnan().all() and dx.isnan().all()
+    assert binding.ffn_fwd(x, wg, wu, wd, act).isnan().all()
+    binding.check_status()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_no_rows(dev, dtype):
     x, wg, wu, wd, dy = _case(0, 64, 128, dtype, dev)
     got = _run(x, wg, wu, wd, dy, "silu")

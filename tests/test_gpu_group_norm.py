@@ -292,6 +292,27 @@ def test_malformed_offsets_of_many_graphs_are_reported(dev, at):
     binding.check_status()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("sizes,C", [([300, 45], 64), ([90000], 128)])
+def test_a_channel_without_a_number_stays_alone(dev, dtype, act, sizes, C):
+    x, w, b, dy, off = _case(sizes, C, dtype, dev)
+    y, mean, rstd = binding.group_norm_fwd(x, w, b, 4, 1e-5, act, off)
+    _, dw, db = binding.group_norm_bwd(dy, x, w, b, mean, rstd, 4, act, off)
+    for value in (float("nan"), float("inf"), -float("inf")):
+        v, bad = b.clone(), (6, 33)
+        v[list(bad)] = value
+        yv, mv, rv = binding.group_norm_fwd(x, w, v, 4, 1e-5, act, off)
+        _, dwv, dbv = binding.group_norm_bwd(dy, x, w, v, mean, rstd, 4, act, off)
+        rest = [c for c in range(C) if c not in bad]
+        assert torch.equal(yv[:, rest], y[:, rest])
+        assert torch.equal(mv, mean) and torch.equal(rv, rstd)
+        assert torch.equal(dwv[rest], dw[rest]) and torch.equal(dbv[rest], db[rest])
+        if value != value:
+            assert yv[:, list(bad)].isnan().all()
+    binding.check_status()
+
+
 def test_no_nodes(dev):
     x = torch.empty((0, 64), device=dev)
     w, b = torch.ones(64, device=dev), torch.zeros(64, device=dev)
