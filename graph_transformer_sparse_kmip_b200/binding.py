@@ -1,5 +1,7 @@
 """Thin ctypes binding of libkmip (the C ABI declared in include/kmip.h).
 
+The attention's calls go through ctypes, those of the operators around it
+through a compiled module (csrc/kmip_host.cpp).
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of libkmip.so.  torch provides device memory and streams.  There is
 no CPU fallback -- if the library is missing, or the tensors are not on a
@@ -21,7 +23,6 @@ LIB_PATH = os.path.join(_PKG, "libkmip_debug.so" if os.environ.get("KMIP_DEBUG_B
 _NVTX = os.environ.get("KMIP_NVTX") == "1"
 
 KMIP_BF16, KMIP_F32 = 0, 1
-POS_TYPES = {torch.float32: 0, torch.int32: 1, torch.int64: 2}
 ACTS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
 STATUS_NAMES = {0: "KMIP_OK", 1: "KMIP_ERR_INVALID_ARG", 2: "KMIP_ERR_UNSUPPORTED",
                 3: "KMIP_ERR_CUDA", 4: "KMIP_ERR_BAD_OFFSETS", 5: "KMIP_ERR_TIMEOUT",
@@ -315,24 +316,31 @@ def attn_bwd(dOut, Q, K, V, idx, lse, scale: float, stream=None, deterministic=F
 
 # --- the operators around the attention: positions, norm, feed-forward ---
 
-# A small call is bound by what happens before its launch: these helpers stay
-# with integers (device indices, addresses, raw stream handles) and make no
-# torch.device, torch.cuda.Stream or ctypes objects on the way.
+# A small call is bound by what happens before its launch, so the checks of
+# tensors, the allocation of results and the call itself are compiled
+# (csrc/kmip_host.cpp): a rotary call on one node takes 7 us, not 12.  KmipError comes from a status, ValueError and TypeError from the
+# checks.
 
-def _same_device(x, *ts):
-    """Every tensor on x's CUDA device and contiguous (x itself may be
-    strided)."""
-    dev = x.get_device()
-    if dev < 0:
-        raise ValueError("libkmip takes CUDA tensors")
-    for t in ts:
-        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
-            raise ValueError(f"expected a contiguous tensor on {x.device}")
+_host = None
+_HOST_CALLS = ("kmip_rotary", "kmip_group_norm_fwd", "kmip_group_norm_bwd", "kmip_ffn_fwd",
+               "kmip_ffn_bwd")
 
 
-def _expect(t, name, shape, dtype):
-    if t is not None and (t.shape != shape or t.dtype != dtype):
-        raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+def load_host():
+    """Load the compiled host module (raises if it has not been built) and
+    hand it the entry points of the loaded library."""
+    global _host
+    if _host is None:
+        lib = load()
+        try:
+            from . import _kmip_host
+        except ImportError as e:
+            raise ImportError(f"the host module cannot be loaded ({e}); build it with "
+                              "`python -m graph_transformer_sparse_kmip_b200.build`") from e
+        _kmip_host.setup(KmipError, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                                      for name in _HOST_CALLS))
+        _host = _kmip_host
+    return _host
 
 
 def _act_code(act: str) -> int:
@@ -341,45 +349,22 @@ def _act_code(act: str) -> int:
     return ACTS[act]
 
 
-def _offsets(graph_offsets):
-    """Checks graph_offsets (int32 [G+1] or None); returns G."""
-    if graph_offsets is None:
-        return 1
-    shape = graph_offsets.shape
-    if graph_offsets.dtype != torch.int32 or len(shape) != 1 or shape[0] < 2:
-        raise ValueError("graph_offsets: expected int32 [G + 1] with G >= 1")
-    return shape[0] - 1
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-
-
-def _launch(x, name, stream, args, tail, *used):
-    """Calls entry point `name` with args, the stream and tail, with x's
-    device current: on `stream`, or on that device's current stream.  Raises
-    on a status.  `used` (and x): the call's tensors, which torch's allocator
-    is told of when the call goes to a stream that is not theirs."""
-    dev = x.get_device()
-    if dev != _device():
-        with torch.cuda.device(dev):
-            return _launch(x, name, stream, args, tail, *used)
-    if stream is not None:
-        s = stream.cuda_stream
-        for t in (x, *used):
-            if t is not None:
-                t.record_stream(stream)
-    elif _raw_stream is not None:
-        s = _raw_stream(dev)
-    else:
-        s = torch.cuda.current_stream().cuda_stream
-    rc = _call(name, *args, s, *tail) if _NVTX else getattr(_lib or load(), name)(*args, s, *tail)
-    if rc:
-        raise KmipError(rc, name)
+def _aside(fn, stream, *args):
+    """fn(*args, stream) in an NVTX range if KMIP_NVTX=1; on a stream that is
+    given, torch's allocator is told of the call's tensors."""
+    outs = ()
+    if _NVTX:
+        torch.cuda.nvtx.range_push("kmip_" + fn.__name__)
+    try:
+        outs = fn(*args, None if stream is None else stream.cuda_stream)
+    finally:
+        if _NVTX:
+            torch.cuda.nvtx.range_pop()
+        if stream is not None:
+            for t in (*args, *(outs if isinstance(outs, tuple) else (outs,))):
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(stream)
+    return outs
 
 
 def rotary(x, pos, freq, axis, inverse: bool = False, interleaved: bool = False, out=None,
@@ -391,30 +376,10 @@ def rotary(x, pos, freq, axis, inverse: bool = False, interleaved: bool = False,
     head adjacent; pos: [N, A] fp32, int32 or int64; freq: fp64 [P]; axis:
     int32 [P].  out: a new contiguous tensor, or a tensor like x (x itself:
     in place).  inverse=True is the gradient with respect to x."""
-    if x.dim() != 3:
-        raise ValueError("x: expected [N, H, d]")
-    (N, H, d), xs, P = x.shape, x.stride(), freq.numel()
-    if xs[2] != 1 and d > 1 and N * H:
-        raise ValueError("x: expected adjacent elements in a head")
-    pos_type = POS_TYPES.get(pos.dtype)
-    if pos_type is None:
-        raise TypeError(f"unsupported position dtype {pos.dtype} (fp32, int32 or int64)")
-    if pos.dim() != 2 or pos.shape[0] != N:
-        raise ValueError(f"pos: expected [{N}, axes], got {tuple(pos.shape)}")
-    _expect(freq, "freq", (P,), torch.float64)
-    _expect(axis, "axis", (P,), torch.int32)
-    _same_device(x, pos, freq, axis)
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    elif (out.shape != x.shape or out.dtype != x.dtype or out.device != x.device
-          or (out.stride(2) != 1 and d > 1 and N * H)):
-        raise ValueError("out: expected a tensor like x")
-    os = out.stride()
-    _launch(x, "kmip_rotary", stream,
-            (x.data_ptr(), xs[0], xs[1], pos.data_ptr(), pos_type, pos.shape[1], freq.data_ptr(),
-             axis.data_ptr(), P, bool(interleaved), bool(inverse), N, H, d, out.data_ptr(), os[0],
-             os[1]), (dtype_code(x.dtype),), pos, freq, axis, out)
-    return out
+    fn = (_host or load_host()).rotary
+    if stream is not None or _NVTX:
+        return _aside(fn, stream, x, pos, freq, axis, inverse, interleaved, out)
+    return fn(x, pos, freq, axis, inverse, interleaved, out, None)
 
 
 def group_norm_fwd(x, weight, bias, groups: int, eps: float = 1e-5, act: str = "none",
@@ -424,83 +389,38 @@ def group_norm_fwd(x, weight, bias, groups: int, eps: float = 1e-5, act: str = "
     x: [N, C] bf16 or fp32, contiguous; weight, bias: [C] like x, or both
     None; graph_offsets: int32 [G+1] or None (one graph).  Returns (y,
     mean, rstd), the last two fp32 [G, groups]."""
-    if x.dim() != 2:
-        raise ValueError("x: expected [N, C]")
-    N, C = x.shape
-    G = _offsets(graph_offsets)
-    _same_device(x, x, weight, bias, graph_offsets)
-    _expect(weight, "weight", (C,), x.dtype)
-    _expect(bias, "bias", (C,), x.dtype)
-    y = torch.empty_like(x)
-    mean = x.new_empty((G, groups), dtype=torch.float32)
-    rstd = torch.empty_like(mean)
-    _launch(x, "kmip_group_norm_fwd", stream,
-            (x.data_ptr(), _addr(weight), _addr(bias), _addr(graph_offsets), N, C, groups, eps,
-             _act_code(act), y.data_ptr(), mean.data_ptr(), rstd.data_ptr()),
-            (G, dtype_code(x.dtype)), weight, bias, graph_offsets, y, mean, rstd)
-    return y, mean, rstd
+    fn = (_host or load_host()).group_norm_fwd
+    if stream is not None or _NVTX:
+        return _aside(fn, stream, x, weight, bias, groups, eps, _act_code(act), graph_offsets)
+    return fn(x, weight, bias, groups, eps, _act_code(act), graph_offsets, None)
 
 
 def group_norm_bwd(dy, x, weight, bias, mean, rstd, groups: int, act: str = "none",
                    graph_offsets=None, stream=None):
     """Backward of group_norm_fwd: (dx, dweight, dbias) in x's type; the last
     two are None when there is no weight."""
-    if x.dim() != 2:
-        raise ValueError("x: expected [N, C]")
-    N, C = x.shape
-    G = _offsets(graph_offsets)
-    _same_device(x, x, dy, weight, bias, graph_offsets, mean, rstd)
-    _expect(dy, "dy", (N, C), x.dtype)
-    _expect(weight, "weight", (C,), x.dtype)
-    _expect(bias, "bias", (C,), x.dtype)
-    _expect(mean, "mean", (G, groups), torch.float32)
-    _expect(rstd, "rstd", (G, groups), torch.float32)
-    dx = torch.empty_like(x)
-    dw = db = None
-    if weight is not None:
-        dw, db = torch.empty_like(weight), torch.empty_like(weight)
-    _launch(x, "kmip_group_norm_bwd", stream,
-            (dy.data_ptr(), x.data_ptr(), _addr(weight), _addr(bias), _addr(graph_offsets),
-             mean.data_ptr(), rstd.data_ptr(), N, C, groups, _act_code(act), dx.data_ptr(),
-             _addr(dw), _addr(db)), (G, dtype_code(x.dtype)), dy, weight, bias, graph_offsets,
-            mean, rstd, dx, dw, db)
-    return dx, dw, db
-
-
-def _ffn_args(x, wg, wu, wd):
-    if x.dim() != 2 or wg.dim() != 2:
-        raise ValueError("x: expected [N, C]; wg, wu: [F, C]; wd: [C, F]")
-    (N, C), F = x.shape, wg.shape[0]
-    _same_device(x, x, wg, wu, wd)
-    _expect(wg, "wg", (F, C), x.dtype)
-    _expect(wu, "wu", (F, C), x.dtype)
-    _expect(wd, "wd", (C, F), x.dtype)
-    return N, C, F
+    fn = (_host or load_host()).group_norm_bwd
+    if stream is not None or _NVTX:
+        return _aside(fn, stream, dy, x, weight, bias, mean, rstd, groups, _act_code(act),
+                      graph_offsets)
+    return fn(dy, x, weight, bias, mean, rstd, groups, _act_code(act), graph_offsets, None)
 
 
 def ffn_fwd(x, wg, wu, wd, act: str = "silu", stream=None):
     """Gated feed-forward block y = (act(x wg^T) * (x wu^T)) wd^T
     (kmip_ffn_fwd).  x: [N, C] bf16 or fp32; wg, wu: [F, C]; wd: [C, F]."""
-    N, C, F = _ffn_args(x, wg, wu, wd)
-    y = torch.empty_like(x)
-    _launch(x, "kmip_ffn_fwd", stream,
-            (x.data_ptr(), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(), N, C, F, _act_code(act),
-             y.data_ptr()), (dtype_code(x.dtype),), wg, wu, wd, y)
-    return y
+    fn = (_host or load_host()).ffn_fwd
+    if stream is not None or _NVTX:
+        return _aside(fn, stream, x, wg, wu, wd, _act_code(act))
+    return fn(x, wg, wu, wd, _act_code(act), None)
 
 
 def ffn_bwd(dy, x, wg, wu, wd, act: str = "silu", stream=None):
     """Backward of ffn_fwd: (dx, dwg, dwu, dwd) in x's type."""
-    N, C, F = _ffn_args(x, wg, wu, wd)
-    _same_device(x, dy)
-    _expect(dy, "dy", (N, C), x.dtype)
-    dx = torch.empty_like(x)
-    dwg, dwu, dwd = torch.empty_like(wg), torch.empty_like(wu), torch.empty_like(wd)
-    _launch(x, "kmip_ffn_bwd", stream,
-            (dy.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(), N, C, F,
-             _act_code(act), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr()),
-            (dtype_code(x.dtype),), dy, wg, wu, wd, dx, dwg, dwu, dwd)
-    return dx, dwg, dwu, dwd
+    fn = (_host or load_host()).ffn_bwd
+    if stream is not None or _NVTX:
+        return _aside(fn, stream, dy, x, wg, wu, wd, _act_code(act))
+    return fn(dy, x, wg, wu, wd, _act_code(act), None)
 
 
 def check_status(stream=None):

@@ -6,6 +6,8 @@ Each ``csrc/*.cu`` compiles to an object under ``_build/`` (skipped when the
 object is newer than every source and header), then all objects link into
 ``graph_transformer_sparse_kmip_b200/libkmip.so`` with the CUDA runtime
 linked statically, so the library needs only the driver at run time.
+``csrc/kmip_host.cpp`` becomes ``_kmip_host.so``, the module through which
+binding.py calls the operators around the attention (g++, torch's headers).
 
 ``--debug-bounds`` builds ``libkmip_debug.so`` instead (objects under
 ``_build/debug/``) with KMIP_DEBUG_BOUNDS defined: the kernels then check
@@ -21,6 +23,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,7 +31,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkmip.so")
 LIB_DEBUG = os.path.join(PKG, "libkmip_debug.so")
+HOST = os.path.join(PKG, "_kmip_host.so")
 NVCC = os.environ.get("NVCC", "nvcc")
+CXX = os.environ.get("CXX", "g++")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -60,13 +65,36 @@ def _compile(src: str, force: bool, verbose: bool, debug: bool = False) -> str:
     return obj
 
 
+def _build_host(force: bool) -> None:
+    src = os.path.join(CSRC, "kmip_host.cpp")
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(ROOT, "include", "kmip.h")))
+    if not force and os.path.exists(HOST) and os.path.getmtime(HOST) >= newest:
+        return
+    import torch
+    from torch.utils import cpp_extension
+    dirs = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"],
+            *cpp_extension.include_paths(device_type="cuda")]
+    tmp = f"{HOST}.{os.getpid()}.tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(f for d in dirs for f in ("-isystem" if "torch" in d else "-I", d)), src, "-o", tmp,
+           *(f"-L{d}" for d in cpp_extension.library_paths()), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, HOST)
+
+
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False,
           debug_bounds: bool = False) -> str:
     os.makedirs(os.path.join(BUILD, "debug") if debug_bounds else BUILD, exist_ok=True)
     lib = LIB_DEBUG if debug_bounds else LIB
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=jobs or min(8, os.cpu_count() or 1)) as ex:
+        host = ex.submit(_build_host, force)
         objs = list(ex.map(lambda s: _compile(s, force, verbose, debug_bounds), srcs))
+        host.result()
     if force or not os.path.exists(lib) or os.path.getmtime(lib) < max(os.path.getmtime(o) for o in objs):
         cmd = [NVCC, *ARCH, "-shared", "-cudart", "static", "-o", lib, *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)

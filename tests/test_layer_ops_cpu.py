@@ -135,6 +135,31 @@ def test_binding_refuses_what_it_cannot_pass():
         binding.ffn_fwd(y, g[0], g, d)
 
 
+def test_host_module_refuses_what_is_not_a_tensor(lib):
+    x, w = torch.zeros(4, 32), torch.zeros(64, 32)
+    h = torch.zeros(4, 2, 32)
+    for call in (lambda: binding.rotary(h, None, None, None),
+                 lambda: binding.rotary([0.0], h, h, h),
+                 lambda: binding.group_norm_fwd(x, 1.0, None, 4),
+                 lambda: binding.group_norm_fwd(x, None, None, "4"),
+                 lambda: binding.group_norm_fwd(x, None, None, 4, "small"),
+                 lambda: binding.group_norm_bwd(None, x, None, None, x, x, 4),
+                 lambda: binding.ffn_fwd(x, w, w, None),
+                 lambda: binding.ffn_bwd(None, x, w, w, w.T.contiguous()),
+                 lambda: binding.load_host().rotary(h)):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: binding.group_norm_fwd(h, None, None, 4),
+                 lambda: binding.group_norm_fwd(x, None, None, -4),
+                 lambda: binding.group_norm_fwd(x, None, None, 1 << 31),
+                 lambda: binding.group_norm_fwd(x, None, None, 4, act="tanh"),
+                 lambda: binding.group_norm_fwd(x, None, None, 4, graph_offsets=torch.zeros(3)),
+                 lambda: binding.ffn_fwd(h, w, w, w),
+                 lambda: binding.ffn_fwd(x, w, w, w.T.contiguous())):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_rotary_tables_made_in_inference_mode_can_train():
     """A layer that answers first and trains later keeps its tables."""
     from graph_transformer_sparse_kmip_b200.layer import AxisRotary
