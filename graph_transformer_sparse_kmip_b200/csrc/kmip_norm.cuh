@@ -17,7 +17,7 @@
 // Two ways over the graphs, chosen by size in plan():
 //   resident  one block per (graph, slab), one launch, for inputs that fit in
 //             L2 and where launches are what costs.  A graph of up to HOLD TY
-//             rows (512 or 1,024) stays in the threads' registers: sum, then
+//             rows (512 or 1,024) stays in registers or shared memory: sum, then
 //             squared deviations from the mean, then the result, with one read
 //             of x.  Longer ones are read again.
 //   split     rows of each graph cut into slots of R rows; one launch writes

@@ -3,7 +3,8 @@
 //
 // Two shapes of block: 256 threads that hold up to eight rows each, and, when
 // there are fewer blocks than SMs, 1,024 threads that hold up to two (one
-// graph of 1,024 x 32 fp32: a quarter of the steps in a row).
+// graph of 1,024 x 32 fp32: a quarter of the steps in a row; 5.4 us on the
+// device, 6.5 with registers instead of shared memory to hold them).
 #include "kmip_launch.cuh"
 #include "kmip_norm.cuh"
 
@@ -54,9 +55,43 @@ __device__ __forceinline__ float group_sum(const NormParams& p, const Slab& s, f
   return sums[min(s.tx / w, s.ngroups - 1)];
 }
 
-template <typename T, int V, int ACT, int NT, int HOLD>
-__global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_fwd_resident(const NormParams p) {
+// A thread's rows of IN inputs between the passes over them, in registers or
+// (16-byte vectors only) in shared memory.  Registers start on the first row
+// as soon as it is there, but every pass is unrolled over all rows, code that
+// runs once a graph and comes from memory.  Shared memory leaves room for more
+// blocks an SM.
+template <typename T, int V, int IN, int NT, int HOLD, bool SHARED>
+struct Held {
+  Row<T, V> rows[HOLD][IN];
+  __device__ explicit Held(void*) {}
+  __device__ void fetch(int u, int i, const T* from) { rows[u][i].load(from); }
+  __device__ void landed() {}
+  __device__ Row<T, V> get(int u, int i) const { return rows[u][i]; }
+};
+template <typename T, int V, int IN, int NT, int HOLD>
+struct Held<T, V, IN, NT, HOLD, true> {
+  uint4* at;  // [HOLD][IN][NT], this thread's column
+  __device__ explicit Held(void* shared) : at(static_cast<uint4*>(shared) + threadIdx.x) {}
+  __device__ void fetch(int u, int i, const T* from) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(at + (u * IN + i) * NT));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  }
+  __device__ void landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+  __device__ Row<T, V> get(int u, int i) const {
+    Row<T, V> r;
+    r.raw = at[(u * IN + i) * NT];
+    return r;
+  }
+};
+template <typename T, int V>
+constexpr bool kWide = sizeof(T) * V == 16;
+
+template <typename T, int V, int ACT, int NT, int HOLD, bool SHARED>
+__global__ void __launch_bounds__(NT, NT == 1024 ? 1 : SHARED ? 4 : 2)
+norm_fwd_resident(const NormParams p) {
   after_previous();
+  constexpr int kUnroll = SHARED ? 2 : HOLD;
+  extern __shared__ float4 dyn[];
   __shared__ StatSmem<NT> sm;
   const Slab s = make_slab<NT, V>(p, blockIdx.y);
   for (int g = blockIdx.x; g < p.G; g += gridDim.x) {
@@ -70,22 +105,23 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_fwd_resident(const
       // (32 bits do: resident inputs are small)
       const int first = (lo + s.ty) * p.C + c, step = s.TY * p.C;
       const T* src = static_cast<const T*>(p.x);
-      Row<T, V> x[HOLD];
+      Held<T, V, 1, NT, HOLD, SHARED> held(dyn);
 #pragma unroll
       for (int u = 0; u < HOLD; ++u)
-        if (u * s.TY < mine) x[u].load(src + (first + u * step));
+        if (u * s.TY < mine) held.fetch(u, 0, src + (first + u * step));
       float2 sum = splat2(0.f), dev = sum;
-#pragma unroll
+      held.landed();
+#pragma unroll kUnroll
       for (int u = 0; u < HOLD; ++u)
-        if (u * s.TY < mine) add_deviations<T, V>(x[u], 0.f, sum, dev);
+        if (u * s.TY < mine) add_deviations<T, V>(held.get(u, 0), 0.f, sum, dev);
       const float count = (float)rows * (float)p.cg;
       float* v0 = reinterpret_cast<float*>(sm.s0);
       float* v1 = reinterpret_cast<float*>(sm.q);
       const float m = group_sum<V, NT>(p, s, sum.x + sum.y, v0, sm.mean) / count;
       dev = sum = splat2(0.f);
-#pragma unroll
+#pragma unroll kUnroll
       for (int u = 0; u < HOLD; ++u)
-        if (u * s.TY < mine) add_deviations<T, V>(x[u], m, sum, dev);
+        if (u * s.TY < mine) add_deviations<T, V>(held.get(u, 0), m, sum, dev);
       const float var = group_sum<V, NT>(p, s, dev.x + dev.y, v1, sm.rstd) / count;
       const float rs = 1.f / sqrtf(var + p.eps);
       if (s.ty == 0 && s.tx * V % p.cg == 0) {
@@ -95,11 +131,12 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_fwd_resident(const
       Forward<T, V> fw;
       fw.set(p, c, m, rs);
       T* out = static_cast<T*>(p.y);
-#pragma unroll
+#pragma unroll kUnroll
       for (int u = 0; u < HOLD; ++u)
         if (u * s.TY < mine) {
-          fw.template apply<ACT>(x[u]);
-          x[u].store(out + (first + u * step), 0);
+          Row<T, V> x = held.get(u, 0);
+          fw.template apply<ACT>(x);
+          x.store(out + (first + u * step), 0);
         }
       __syncthreads();
       continue;
@@ -120,10 +157,14 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_fwd_resident(const
 }
 
 template <typename T, int V, int ACT, int NT, int HOLD>
-__global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_bwd_resident(const NormParams p) {
+__global__ void __launch_bounds__(NT, NT == 1024 ? 1 : 2) norm_bwd_resident(const NormParams p) {
   after_previous();
   extern __shared__ float4 dyn[];
-  BwdSmem<NT, V>& sm = *reinterpret_cast<BwdSmem<NT, V>*>(dyn);
+  // Two inputs do not fit in registers beside the sums: 256 graphs of 450 x 128
+  // bf16 took 55 us so, 38 with shared memory, 64 graphs 18.6 and 15.3.
+  constexpr int kUnroll = kWide<T, V> ? 2 : HOLD;
+  BwdSmem<NT, V>& sm =
+      *reinterpret_cast<BwdSmem<NT, V>*>(dyn + (kWide<T, V> ? HOLD * 2 * NT : 0));
   __shared__ float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
   const Slab s = make_slab<NT, V>(p, blockIdx.y);
   float* dst = p.chan + (int64_t)blockIdx.x * 2 * p.C;
@@ -139,12 +180,12 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_bwd_resident(const
       const int first = (lo + s.ty) * p.C + c, step = s.TY * p.C;
       const T* src = static_cast<const T*>(p.x);
       const T* gsrc = static_cast<const T*>(p.dy);
-      Row<T, V> x[HOLD], dy[HOLD];
+      Held<T, V, 2, NT, HOLD, kWide<T, V>> held(dyn);
 #pragma unroll
       for (int u = 0; u < HOLD; ++u)
         if (u * s.TY < mine) {
-          x[u].load(src + (first + u * step));
-          dy[u].load(gsrc + (first + u * step));
+          held.fetch(u, 0, src + (first + u * step));
+          held.fetch(u, 1, gsrc + (first + u * step));
         }
       Backward<T, V> bw;
       bw.set(p, c, p.mean[(int64_t)g * p.groups + s.g0 + j],
@@ -154,11 +195,12 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_bwd_resident(const
         float2 sdb[P], sdw[P];
 #pragma unroll
         for (int e = 0; e < P; ++e) sdb[e] = sdw[e] = splat2(0.f);
-#pragma unroll
+        held.landed();
+#pragma unroll kUnroll
         for (int u = 0; u < HOLD; ++u)
           if (u * s.TY < mine) {
             float2 xh[P], dz[P];
-            bw.template rows<ACT>(x[u], dy[u], xh, dz);
+            bw.template rows<ACT>(held.get(u, 0), held.get(u, 1), xh, dz);
 #pragma unroll
             for (int e = 0; e < P; ++e) {
               sdb[e] = vadd<V>(sdb[e], dz[e]);
@@ -171,11 +213,12 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_bwd_resident(const
       const float inv = rows ? 1.f / ((float)rows * (float)p.cg) : 0.f;
       const float a1 = (float)sm.gm1[j] * inv, a2 = (float)sm.gm2[j] * inv;
       T* out = static_cast<T*>(p.dx);
-#pragma unroll
+#pragma unroll kUnroll
       for (int u = 0; u < HOLD; ++u)
         if (u * s.TY < mine) {
-          bw.template apply<ACT>(x[u], dy[u], a1, a2);
-          dy[u].store(out + (first + u * step), 0);
+          Row<T, V> dy = held.get(u, 1);
+          bw.template apply<ACT>(held.get(u, 0), dy, a1, a2);
+          dy.store(out + (first + u * step), 0);
         }
       __syncthreads();
       continue;
@@ -213,29 +256,39 @@ int norm_resident_blocks(const NormParams& p, int slabs) {
 cudaError_t launch_norm_fwd_resident(kmip_dtype_t dtype, int v, int act, const NormParams& p,
                                      int slabs, cudaStream_t stream) {
   return norm_dispatch(dtype, v, act, [&]<typename T, int V, int ACT>() {
-    if (few_blocks(p, slabs))
-      norm_fwd_resident<T, V, ACT, 1024, 2><<<resident_grid(p, slabs), 1024, 0, stream>>>(p);
-    else
-      norm_fwd_resident<T, V, ACT, 256, 8><<<resident_grid(p, slabs), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    const auto run = [&]<int NT, int HOLD, bool SHARED>() {
+      auto kern = norm_fwd_resident<T, V, ACT, NT, HOLD, SHARED>;
+      constexpr int smem = SHARED ? HOLD * NT * 16 : 0;
+      const cudaError_t e =
+          cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      kern<<<resident_grid(p, slabs), NT, smem, stream>>>(p);
+      return cudaGetLastError();
+    };
+    // Shared memory where blocks wait for one another (48,660 x 128 bf16 in 2,000
+    // graphs 18.7 us, with registers 21.5), registers where all run at once
+    // (28,072 x 128 in 64 graphs 8.0 us, with shared memory 10.2).
+    if (few_blocks(p, slabs)) return run.template operator()<1024, 2, kWide<T, V>>();
+    if (kWide<T, V> && (int64_t)p.G * slabs > 2 * device_sm_count())
+      return run.template operator()<256, 8, kWide<T, V>>();
+    return run.template operator()<256, 8, false>();
   });
 }
 
 cudaError_t launch_norm_bwd_resident(kmip_dtype_t dtype, int v, int act, const NormParams& p,
                                      int slabs, cudaStream_t stream) {
   return norm_dispatch(dtype, v, act, [&]<typename T, int V, int ACT>() {
-    if (few_blocks(p, slabs)) {
-      auto kern = norm_bwd_resident<T, V, ACT, 1024, 2>;
-      constexpr int smem = sizeof(BwdSmem<1024, V>);
+    const auto run = [&]<int NT, int HOLD>() {
+      auto kern = norm_bwd_resident<T, V, ACT, NT, HOLD>;
+      constexpr int smem = (kWide<T, V> ? HOLD * 2 * NT * 16 : 0) + (int)sizeof(BwdSmem<NT, V>);
       const cudaError_t e =
           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
-      kern<<<resident_grid(p, slabs), 1024, smem, stream>>>(p);
-    } else {
-      norm_bwd_resident<T, V, ACT, 256, 8>
-          <<<resident_grid(p, slabs), 256, sizeof(BwdSmem<256, V>), stream>>>(p);
-    }
-    return cudaGetLastError();
+      kern<<<resident_grid(p, slabs), NT, smem, stream>>>(p);
+      return cudaGetLastError();
+    };
+    return few_blocks(p, slabs) ? run.template operator()<1024, 2>()
+                                : run.template operator()<256, 8>();
   });
 }
 
