@@ -165,6 +165,16 @@ def test_single_node(dev):
     _check(x, w, b, dy, off, 2, "silu")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("C,groups", [(64, 4), (128, 4), (40, 8)])
+def test_more_graphs_than_blocks_fit(dev, dtype, C, groups):
+    """Graphs that are kept on the chip and longer ones, several waves of blocks."""
+    g = torch.Generator().manual_seed(5)
+    sizes = [0, 1, 511, 512, 513] + [int(v) for v in torch.randint(0, 700, (320,), generator=g)]
+    x, w, b, dy, off = _case(sizes, C, dtype, dev, seed=6)
+    _check(x, w, b, dy, off, groups, "silu")
+
+
 def test_many_tiny_graphs(dev):
     sizes = [int(v) for v in torch.randint(0, 9, (5000,), generator=torch.Generator().manual_seed(2))]
     x, w, b, dy, off = _case(sizes, 64, F32, dev, seed=4)

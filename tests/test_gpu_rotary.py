@@ -191,3 +191,21 @@ def test_empty_stream_and_graph_capture(dev):
     graph.replay()
     torch.cuda.synchronize()
     _check(out, *_reference(x, pos, freq, axis, False, False))
+
+
+def test_out_is_returned_and_checked(dev):
+    x = torch.randn((5, 2, 32), device=dev)
+    pos, freq = torch.zeros((5, 1), device=dev), torch.ones(16, dtype=torch.float64, device=dev)
+    axis = torch.zeros(16, dtype=torch.int32, device=dev)
+    assert binding.rotary(x, pos, freq, axis, out=x) is x
+    y = torch.empty_like(x)
+    assert binding.rotary(x, pos, freq, axis, out=y, stream=torch.cuda.current_stream()) is y
+    assert torch.equal(x, y)
+    for out in (y[:4], y.bfloat16(), y.cpu(), y[0], y.transpose(1, 2)):
+        with pytest.raises(ValueError, match="out"):
+            binding.rotary(x, pos, freq, axis, out=out)
+    with pytest.raises(ValueError, match="contiguous"):
+        binding.rotary(x, pos, freq.cpu(), axis)
+    with pytest.raises(TypeError, match="dtype"):
+        binding.rotary(x.double(), pos, freq, axis)
+    binding.check_status()
