@@ -118,6 +118,30 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on(stream, fn, *args):
+    """fn(*args) with `stream` as the current stream.  The results come from
+    that stream's memory, so it may write them at once (memory of the caller's
+    stream may still be in use there); torch's allocator is told that the
+    arguments are used on `stream` and the results by the caller's."""
+    tensors = [t for t in args if isinstance(t, torch.Tensor) and t.is_cuda]
+    for t in tensors:
+        if t.device != stream.device:
+            raise ValueError(f"tensor on {t.device}, stream on {stream.device}")
+    caller = torch.cuda.current_stream(stream.device)
+    outs = ()
+    try:
+        with torch.cuda.stream(stream):
+            outs = fn(*args)
+    finally:
+        if stream != caller:
+            for t in tensors:
+                t.record_stream(stream)
+            for t in outs if isinstance(outs, tuple) else (outs,):
+                if t is not None:
+                    t.record_stream(caller)
+    return outs
+
+
 def dtype_code(t: torch.dtype) -> int:
     if t == torch.bfloat16:
         return KMIP_BF16
@@ -350,21 +374,14 @@ def _act_code(act: str) -> int:
 
 
 def _aside(fn, stream, *args):
-    """fn(*args, stream) in an NVTX range if KMIP_NVTX=1; on a stream that is
-    given, torch's allocator is told of the call's tensors."""
-    outs = ()
+    """fn(*args) in an NVTX range if KMIP_NVTX=1, on `stream` if one is given."""
     if _NVTX:
         torch.cuda.nvtx.range_push("kmip_" + fn.__name__)
     try:
-        outs = fn(*args, None if stream is None else stream.cuda_stream)
+        return fn(*args) if stream is None else _on(stream, fn, *args)
     finally:
         if _NVTX:
             torch.cuda.nvtx.range_pop()
-        if stream is not None:
-            for t in (*args, *(outs if isinstance(outs, tuple) else (outs,))):
-                if isinstance(t, torch.Tensor) and t.is_cuda:
-                    t.record_stream(stream)
-    return outs
 
 
 def rotary(x, pos, freq, axis, inverse: bool = False, interleaved: bool = False, out=None,
@@ -379,7 +396,7 @@ def rotary(x, pos, freq, axis, inverse: bool = False, interleaved: bool = False,
     fn = (_host or load_host()).rotary
     if stream is not None or _NVTX:
         return _aside(fn, stream, x, pos, freq, axis, inverse, interleaved, out)
-    return fn(x, pos, freq, axis, inverse, interleaved, out, None)
+    return fn(x, pos, freq, axis, inverse, interleaved, out)
 
 
 def group_norm_fwd(x, weight, bias, groups: int, eps: float = 1e-5, act: str = "none",
@@ -392,7 +409,7 @@ def group_norm_fwd(x, weight, bias, groups: int, eps: float = 1e-5, act: str = "
     fn = (_host or load_host()).group_norm_fwd
     if stream is not None or _NVTX:
         return _aside(fn, stream, x, weight, bias, groups, eps, _act_code(act), graph_offsets)
-    return fn(x, weight, bias, groups, eps, _act_code(act), graph_offsets, None)
+    return fn(x, weight, bias, groups, eps, _act_code(act), graph_offsets)
 
 
 def group_norm_bwd(dy, x, weight, bias, mean, rstd, groups: int, act: str = "none",
@@ -403,7 +420,7 @@ def group_norm_bwd(dy, x, weight, bias, mean, rstd, groups: int, act: str = "non
     if stream is not None or _NVTX:
         return _aside(fn, stream, dy, x, weight, bias, mean, rstd, groups, _act_code(act),
                       graph_offsets)
-    return fn(dy, x, weight, bias, mean, rstd, groups, _act_code(act), graph_offsets, None)
+    return fn(dy, x, weight, bias, mean, rstd, groups, _act_code(act), graph_offsets)
 
 
 def ffn_fwd(x, wg, wu, wd, act: str = "silu", stream=None):
@@ -412,7 +429,7 @@ def ffn_fwd(x, wg, wu, wd, act: str = "silu", stream=None):
     fn = (_host or load_host()).ffn_fwd
     if stream is not None or _NVTX:
         return _aside(fn, stream, x, wg, wu, wd, _act_code(act))
-    return fn(x, wg, wu, wd, _act_code(act), None)
+    return fn(x, wg, wu, wd, _act_code(act))
 
 
 def ffn_bwd(dy, x, wg, wu, wd, act: str = "silu", stream=None):
@@ -420,7 +437,7 @@ def ffn_bwd(dy, x, wg, wu, wd, act: str = "silu", stream=None):
     fn = (_host or load_host()).ffn_bwd
     if stream is not None or _NVTX:
         return _aside(fn, stream, dy, x, wg, wu, wd, _act_code(act))
-    return fn(dy, x, wg, wu, wd, _act_code(act), None)
+    return fn(dy, x, wg, wu, wd, _act_code(act))
 
 
 def check_status(stream=None):

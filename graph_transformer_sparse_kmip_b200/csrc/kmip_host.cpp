@@ -122,21 +122,11 @@ struct Launch {
   explicit Launch(const Tensor& x) : guard(x.device()) {}
 };
 
-// The stream of a raw handle, or the current one.
-struct Stream {
-  bool given;
-  kmip_stream_t handle;
-  explicit Stream(PyObject* o) : given(o != Py_None), handle(nullptr) {
-    if (given) {
-      const unsigned long long v = PyLong_AsUnsignedLongLong(o);
-      if (v == ~0ull && PyErr_Occurred()) throw Raised{};
-      handle = reinterpret_cast<kmip_stream_t>(v);
-    }
-  }
-  kmip_stream_t on(const Tensor& x) const {
-    return given ? handle : c10::cuda::getCurrentCUDAStream(x.get_device()).stream();
-  }
-};
+// The stream that is current on x's device.  Results come from the allocator's
+// pool of that stream, so the stream that writes them has to be this one.
+kmip_stream_t stream_of(const Tensor& x) {
+  return c10::cuda::getCurrentCUDAStream(x.get_device()).stream();
+}
 
 void check(kmip_status_t status, const char* where) {
   if (status != KMIP_OK) throw Failed{status, where};
@@ -170,14 +160,13 @@ PyObject* guarded(Py_ssize_t n, F&& f) {
 }
 
 // ------------------------------------------------------------------ operators
-// rotary(x, pos, freq, axis, inverse, interleaved, out or None, stream or None)
+// rotary(x, pos, freq, axis, inverse, interleaved, out or None)
 PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded<8>(n, [&] {
+  return guarded<7>(n, [&] {
     const Tensor &x = tensor(a[0], "x"), &pos = tensor(a[1], "pos"), &freq = tensor(a[2], "freq"),
                  &axis = tensor(a[3], "axis");
     const bool inverse = truth(a[4]), interleaved = truth(a[5]);
     const Tensor* given = optional(a[6], "out");
-    const Stream stream(a[7]);
     if (x.dim() != 3) refuse("x: expected [N, H, d]");
     const int64_t N = x.size(0), H = x.size(1), d = x.size(2), P = freq.numel();
     const bool any = d > 1 && N > 0 && H > 0;
@@ -209,16 +198,16 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
       check(g_rotary(in(x), x.stride(0), x.stride(1), in(pos), type, axes,
                      static_cast<const double*>(in(freq)), static_cast<const int32_t*>(in(axis)),
                      pairs, interleaved, inverse, N, h, width, out(y), y.stride(0), y.stride(1),
-                     stream.on(x), dtype),
+                     stream_of(x), dtype),
             "kmip_rotary");
     }
     return THPVariable_Wrap(y);
   });
 }
 
-// group_norm_fwd(x, weight, bias, groups, eps, act, graph_offsets, stream)
+// group_norm_fwd(x, weight, bias, groups, eps, act, graph_offsets)
 PyObject* group_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded<8>(n, [&] {
+  return guarded<7>(n, [&] {
     const Tensor& x = tensor(a[0], "x");
     const Tensor *w = optional(a[1], "weight"), *b = optional(a[2], "bias");
     const int groups = narrow(integer(a[3]), "groups");
@@ -226,7 +215,6 @@ PyObject* group_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (eps == -1.0 && PyErr_Occurred()) throw Raised{};
     const int act = narrow(integer(a[5]), "act");
     const Tensor* off = optional(a[6], "graph_offsets");
-    const Stream stream(a[7]);
     if (x.dim() != 2) refuse("x: expected [N, C]");
     const int64_t N = x.size(0), C = x.size(1);
     const int G = graphs(off);
@@ -244,23 +232,21 @@ PyObject* group_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       check(g_norm_fwd(in(x), in(w), in(b), static_cast<const int32_t*>(in(off)), N, channels,
                        groups, (float)eps, (kmip_act_t)act, out(y),
                        static_cast<float*>(out(mean)), static_cast<float*>(out(rstd)),
-                       stream.on(x), G, dtype),
+                       stream_of(x), G, dtype),
             "kmip_group_norm_fwd");
     }
     return tuple({y, mean, rstd});
   });
 }
 
-// group_norm_bwd(dy, x, weight, bias, mean, rstd, groups, act, graph_offsets,
-//                stream)
+// group_norm_bwd(dy, x, weight, bias, mean, rstd, groups, act, graph_offsets)
 PyObject* group_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded<10>(n, [&] {
+  return guarded<9>(n, [&] {
     const Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x");
     const Tensor *w = optional(a[2], "weight"), *b = optional(a[3], "bias");
     const Tensor &mean = tensor(a[4], "mean"), &rstd = tensor(a[5], "rstd");
     const int groups = narrow(integer(a[6]), "groups"), act = narrow(integer(a[7]), "act");
     const Tensor* off = optional(a[8], "graph_offsets");
-    const Stream stream(a[9]);
     if (x.dim() != 2) refuse("x: expected [N, C]");
     const int64_t N = x.size(0), C = x.size(1);
     const int G = graphs(off);
@@ -283,7 +269,7 @@ PyObject* group_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       check(g_norm_bwd(in(dy), in(x), in(w), in(b), static_cast<const int32_t*>(in(off)),
                        static_cast<const float*>(in(mean)), static_cast<const float*>(in(rstd)), N,
                        channels, groups, (kmip_act_t)act, out(dx), w ? out(dw) : nullptr,
-                       w ? out(db) : nullptr, stream.on(x), G, dtype),
+                       w ? out(db) : nullptr, stream_of(x), G, dtype),
             "kmip_group_norm_bwd");
     }
     return tuple({dx, dw, db});
@@ -314,29 +300,27 @@ struct Ffn {
   }
 };
 
-// ffn_fwd(x, wg, wu, wd, act, stream)
+// ffn_fwd(x, wg, wu, wd, act)
 PyObject* ffn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded<6>(n, [&] {
+  return guarded<5>(n, [&] {
     const Ffn p(a);
-    const Stream stream(a[5]);
     Tensor y;
     {
       const Launch launch(p.x);
       y = at::empty(p.x.sizes(), p.x.options());
       check(g_ffn_fwd(in(p.x), in(p.wg), in(p.wu), in(p.wd), p.N, p.c, p.f, p.act, out(y),
-                      stream.on(p.x), p.dtype),
+                      stream_of(p.x), p.dtype),
             "kmip_ffn_fwd");
     }
     return THPVariable_Wrap(y);
   });
 }
 
-// ffn_bwd(dy, x, wg, wu, wd, act, stream)
+// ffn_bwd(dy, x, wg, wu, wd, act)
 PyObject* ffn_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded<7>(n, [&] {
+  return guarded<6>(n, [&] {
     const Tensor& dy = tensor(a[0], "dy");
     const Ffn p(a + 1);
-    const Stream stream(a[6]);
     same_device(p.x, {&dy});
     expect(&dy, "dy", {p.N, p.C}, p.x.scalar_type());
     Tensor dx, dwg, dwu, dwd;
@@ -347,7 +331,7 @@ PyObject* ffn_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       dwu = at::empty(p.wu.sizes(), p.x.options());
       dwd = at::empty(p.wd.sizes(), p.x.options());
       check(g_ffn_bwd(in(dy), in(p.x), in(p.wg), in(p.wu), in(p.wd), p.N, p.c, p.f, p.act, out(dx),
-                      out(dwg), out(dwu), out(dwd), stream.on(p.x), p.dtype),
+                      out(dwg), out(dwu), out(dwd), stream_of(p.x), p.dtype),
             "kmip_ffn_bwd");
     }
     return tuple({dx, dwg, dwu, dwd});
