@@ -248,10 +248,12 @@ def kmip_attn_gather(Q, K, V, idx, N, H, d, k, scale, out, lse, stream=None, dty
 
 def attn_gather(Q, K, V, idx, scale: float, stream=None):
     """Returns (out, lse) of attention over the given sets idx [N, H, k]."""
+    if stream is not None:
+        return _on(stream, attn_gather, Q, K, V, idx, scale)
     N, H, d = Q.shape
     out = torch.empty_like(Q)
     lse = torch.empty((N, H), dtype=torch.float32, device=Q.device)
-    rc = kmip_attn_gather(Q, K, V, idx, N, H, d, idx.shape[-1], scale, out, lse, stream)
+    rc = kmip_attn_gather(Q, K, V, idx, N, H, d, idx.shape[-1], scale, out, lse)
     if rc:
         raise KmipError(rc, "kmip_attn_gather")
     return out, lse
@@ -301,11 +303,13 @@ def kmip_test_wait_timeout(timeout_us: int, stream=None) -> int:
 
 def attn_fwd(Q, K, V, k: int, scale: float, graph_offsets=None, stream=None):
     """Returns (out [N,H,d] like Q, idx [N,H,k] int32, lse [N,H] fp32)."""
+    if stream is not None:
+        return _on(stream, attn_fwd, Q, K, V, k, scale, graph_offsets)
     N, H, d = Q.shape
     out = torch.empty_like(Q)
     idx = torch.empty((N, H, k), dtype=torch.int32, device=Q.device)
     lse = torch.empty((N, H), dtype=torch.float32, device=Q.device)
-    rc = kmip_attn_fwd(Q, K, V, graph_offsets, N, H, d, k, scale, out, idx, lse, stream)
+    rc = kmip_attn_fwd(Q, K, V, graph_offsets, N, H, d, k, scale, out, idx, lse)
     if rc:
         raise KmipError(rc, "kmip_attn_fwd")
     return out, idx, lse
@@ -314,13 +318,14 @@ def attn_fwd(Q, K, V, k: int, scale: float, graph_offsets=None, stream=None):
 def attn_fwd_diag(Q, K, V, k: int, scale: float, graph_offsets=None, stream=None):
     """Returns (out, idx, lse, lse_all): kmip_attn_fwd's outputs and the
     log-sum-exp over every key of the query's graph."""
+    if stream is not None:
+        return _on(stream, attn_fwd_diag, Q, K, V, k, scale, graph_offsets)
     N, H, d = Q.shape
     out = torch.empty_like(Q)
     idx = torch.empty((N, H, k), dtype=torch.int32, device=Q.device)
     lse = torch.empty((N, H), dtype=torch.float32, device=Q.device)
     lse_all = torch.empty((N, H), dtype=torch.float32, device=Q.device)
-    rc = kmip_attn_fwd_diag(Q, K, V, graph_offsets, N, H, d, k, scale, out, idx, lse, lse_all,
-                            stream)
+    rc = kmip_attn_fwd_diag(Q, K, V, graph_offsets, N, H, d, k, scale, out, idx, lse, lse_all)
     if rc:
         raise KmipError(rc, "kmip_attn_fwd_diag")
     return out, idx, lse, lse_all
@@ -328,11 +333,13 @@ def attn_fwd_diag(Q, K, V, k: int, scale: float, graph_offsets=None, stream=None
 
 def attn_bwd(dOut, Q, K, V, idx, lse, scale: float, stream=None, deterministic=False):
     """Returns (dQ, dK, dV), fp32 [N,H,d]."""
+    if stream is not None:
+        return _on(stream, attn_bwd, dOut, Q, K, V, idx, lse, scale, None, deterministic)
     dQ = torch.empty(Q.shape, dtype=torch.float32, device=Q.device)
     dK = torch.empty_like(dQ)
     dV = torch.empty_like(dQ)
     fn = kmip_attn_bwd_deterministic if deterministic else kmip_attn_bwd
-    rc = fn(dOut, Q, K, V, idx, lse, dQ, dK, dV, stream, scale=scale)
+    rc = fn(dOut, Q, K, V, idx, lse, dQ, dK, dV, scale=scale)
     if rc:
         raise KmipError(rc, fn.__name__)
     return dQ, dK, dV

@@ -58,7 +58,13 @@ def _calls(name, dev):
         if "fwd" in name:
             return lambda s: binding.ffn_fwd(x, wg, wu, wd, stream=s)
         return lambda s: binding.ffn_bwd(dy, x, wg, wu, wd, stream=s)
-    raise AssertionError(name)
+    q, k, v, do = (n(300, 2, 32) for _ in range(4))
+    out, idx, lse = binding.attn_fwd(q, k, v, 5, 0.2)
+    return {"attn_fwd": lambda s: binding.attn_fwd(q, k, v, 5, 0.2, stream=s),
+            "attn_fwd_diag": lambda s: binding.attn_fwd_diag(q, k, v, 5, 0.2, stream=s),
+            "attn_gather": lambda s: binding.attn_gather(q, k, v, idx, 0.2, stream=s),
+            "attn_bwd": lambda s: binding.attn_bwd(do, q, k, v, idx, lse, 0.2, stream=s,
+                                                   deterministic=True)}[name]
 
 
 def _check(dev, call):
@@ -80,7 +86,8 @@ def _check(dev, call):
 
 @pytest.mark.parametrize("name", ["rotary", "norm_fwd", "norm_bwd", "norm_fwd_large",
                                   "norm_bwd_large", "ffn_fwd", "ffn_fwd_rows", "ffn_fwd_f32",
-                                  "ffn_bwd", "ffn_bwd_f32"])
+                                  "ffn_bwd", "ffn_bwd_f32", "attn_fwd", "attn_fwd_diag",
+                                  "attn_gather", "attn_bwd"])
 def test_results_belong_to_the_stream_that_writes_them(dev, name):
     _check(dev, _calls(name, dev))
 
