@@ -44,6 +44,18 @@ __device__ __forceinline__ void warp_sums(float (&v)[N]) {
   }
 }
 
+// Vec<X>::load by a plain load: the second kernel starts before the first has
+// written h, and the read-only path wants memory that no one writes while a
+// kernel lives.
+template <typename X>
+__device__ __forceinline__ void load_row(const X* p, float* f) {
+  if constexpr (sizeof(X) == 4) {
+    *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(p);
+  } else {
+    Vec<X>::load(p, f);  // x, an input
+  }
+}
+
 // Dot products of M weight rows (w[m], length K) with `rows` rows of x (row
 // stride K) over every S-th step from `part` on: acc[m][n], in every lane.
 template <typename T, typename X, int M, int NR>
@@ -71,7 +83,7 @@ __device__ __forceinline__ void dots(const T* const (&w)[M], const X* x, int row
         float v[V];
 #pragma unroll
         for (int e = 0; e < V; e += Vec<X>::N)
-          Vec<X>::load(x + (int64_t)n * K + k0 + b * step + e, v + e);
+          load_row(x + (int64_t)n * K + k0 + b * step + e, v + e);
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll

@@ -191,3 +191,22 @@ def test_side_stream_and_captured_graphs(dev, dtype):
     for _, _, args, got in work:
         for k, v in _run(*args, "silu").items():
             assert torch.equal(v, got[k]), k
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N", [1, 3, 16])
+def test_few_rows_see_the_projections_of_their_own_call(dev, dtype, N):
+    """Calls of a few rows in close succession, each with the scratch of the one
+    before it: the second kernel starts before the first has written."""
+    g = torch.Generator(device=dev).manual_seed(N)
+    _, wg, wu, wd, _ = _case(1, 1024, 2816, dtype, dev)
+    xs = [torch.randn((N, 1024), generator=g, device=dev).to(dtype) for _ in range(8)]
+    want = []
+    for x in xs:
+        want.append(binding.ffn_fwd(x, wg, wu, wd))
+        torch.cuda.synchronize()
+    for _ in range(20):
+        got = [binding.ffn_fwd(x, wg, wu, wd) for x in xs]
+        for a, c in zip(got, want):
+            assert torch.equal(a, c)
+    binding.check_status()
