@@ -68,6 +68,7 @@ constexpr int kStage = kStageA + kStageB;
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = (kEpiWarps + 2) * 32;
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s
+constexpr uint64_t kSettleNs = 10000000ull;     // 10 ms: what is in flight takes microseconds
 
 constexpr int kBox = 32 * 32 * 2;    // a warp's output box
 
@@ -165,7 +166,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
   const uint32_t boxes = base + kStages * kStage;
   const uint32_t bars = boxes + kEpiWarps * boxes_of(MODE) * kBox;
   const uint32_t full = bars, empty = bars + 8 * kStages;
-  const uint32_t tfull = empty + 8 * kStages, tempty = tfull + 16;
+  const uint32_t tfull = empty + 8 * kStages, tempty = tfull + 16, settled = tempty + 16;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_store;
   volatile int* abort_flag = &abort_store;
@@ -173,6 +174,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  uint32_t issued = 0;  // steps that the producer has loaded
 
   if (threadIdx.x == 0) {
     abort_store = 0;
@@ -184,6 +186,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
       mbar_init(tfull + 8 * b, 1);
       mbar_init(tempty + 8 * b, 2 * kEpiWarps);
     }
+    mbar_init(settled, 1);
     fence_mbar_init();
   }
   if (warp == kEpiWarps + 1) {
@@ -202,7 +205,6 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       const uint32_t full0 = map_to_cta(full, 0);
-      uint32_t it_no = 0;
       Walk walk(cluster, clusters, steps);
       Item it;
       bool ok = true;
@@ -210,8 +212,8 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
         const int mt = it.tile / p.tiles_n, nt = it.tile % p.tiles_n;
         for (int seg = 0; seg < kSegs && ok; ++seg) {
           const int kn = seg ? p.kb1 : it.kn;
-          for (int kb = 0; kb < kn; ++kb, ++it_no) {
-            const uint32_t s = it_no % kStages, ph = (it_no / kStages) & 1;
+          for (int kb = 0; kb < kn; ++kb, ++issued) {
+            const uint32_t s = issued % kStages, ph = (issued / kStages) & 1;
             if (!mbar_wait(empty + 8 * s, ph ^ 1, abort_flag, kTimeoutNs)) {
               ok = false;
               break;
@@ -454,6 +456,30 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {
+    // A wait ran out, so work may still be in flight; neither CTA frees tensor
+    // memory or leaves before it has landed, or as long as kSettleNs later.
+    const auto settle = [](uint32_t bar, uint32_t parity) {
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait(bar, parity) && global_ns() - t0 < kSettleNs) {
+      }
+    };
+    if (warp == kEpiWarps && lane == 0) {
+      if (rank == 0) {  // where the copies of both CTAs are counted
+        for (uint32_t s = 0; s < (uint32_t)kStages; ++s)
+          if (issued > s) settle(full + 8 * s, (issued - 1 - s) / kStages & 1);
+      } else {          // copies of a step that the other CTA did not begin
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < kSettleNs) {
+        }
+      }
+    }
+    if (warp == kEpiWarps + 1 && lane == 0) {
+      if (rank == 0) mma_commit_pair(settled);
+      settle(settled, 0);
+    }
+  }
+  __syncwarp();
   cluster_sync();
   if (*abort_flag && threadIdx.x == 0) record_status(p.status, KMIP_ERR_TIMEOUT);
   if (warp == kEpiWarps + 1) {
