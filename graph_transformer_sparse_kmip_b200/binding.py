@@ -396,10 +396,11 @@ def rotary(x, pos, freq, axis, inverse: bool = False, interleaved: bool = False,
     """Rotary positions with several axes (kmip_rotary): pair p of every head
     of node n turns by pos[n, axis[p]] * freq[p].
 
-    x: [N, H, d] bf16 or fp32, rows and heads at any stride, elements of a
-    head adjacent; pos: [N, A] fp32, int32 or int64; freq: fp64 [P]; axis:
-    int32 [P].  out: a new contiguous tensor, or a tensor like x (x itself:
-    in place).  inverse=True is the gradient with respect to x."""
+    x: [N, H, d] bf16 or fp32, rows and heads at any stride (interleaved: an
+    even one, from an address that a pair is aligned to), elements of a head
+    adjacent; pos: [N, A] fp32, int32 or int64; freq: fp64 [P]; axis: int32
+    [P].  out: a new contiguous tensor, or a tensor like x (x itself: in
+    place).  inverse=True is the gradient with respect to x."""
     fn = (_host or load_host()).rotary
     if stream is not None or _NVTX:
         return _aside(fn, stream, x, pos, freq, axis, inverse, interleaved, out)

@@ -61,6 +61,16 @@ def kmip_attention(Q, K, V, k: int, scale: float | None = None, offsets=None):
     return KmipAttentionFunction.apply(Q, K, V, offsets, int(k), float(scale))
 
 
+def _turnable(x, interleaved: bool):
+    """x [N, H, d], or a copy where kmip_rotary cannot take its layout: a
+    head's elements adjacent and, interleaved, every pair aligned as one."""
+    if x.stride(2) != 1 or interleaved and (
+            x.data_ptr() % (2 * x.element_size()) or
+            any(s % 2 for s, n in zip(x.stride()[:2], x.shape) if n > 1)):
+        return x.clone(memory_format=torch.contiguous_format)
+    return x
+
+
 class RotaryFunction(torch.autograd.Function):
     """Autograd wrapper of kmip_rotary: the gradient is the inverse turn.
     Positions and frequencies get no gradient."""
@@ -69,15 +79,15 @@ class RotaryFunction(torch.autograd.Function):
     def forward(ctx, x, pos, freq, axis, interleaved: bool):
         ctx.save_for_backward(pos, freq, axis)
         ctx.interleaved = interleaved
-        return binding.rotary(x, pos, freq, axis, interleaved=interleaved)
+        return binding.rotary(_turnable(x, interleaved), pos, freq, axis,
+                              interleaved=interleaved)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
         pos, freq, axis = ctx.saved_tensors
-        if dout.stride(2) != 1:
-            dout = dout.contiguous()
-        dx = binding.rotary(dout, pos, freq, axis, inverse=True, interleaved=ctx.interleaved)
+        dx = binding.rotary(_turnable(dout, ctx.interleaved), pos, freq, axis, inverse=True,
+                            interleaved=ctx.interleaved)
         return dx, None, None, None, None
 
 

@@ -202,3 +202,30 @@ def test_captured_training_step(dev):
     # dK and dV are fp32 atomic sums whose last bits vary
     assert (dx.float() - dx2.float()).norm() <= 4e-3 * dx2.float().norm()
     assert torch.equal(dgate, dgate2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_of_odd_strides_and_addresses(dev, dtype, interleaved):
+    """Inputs and gradients at odd strides or behind an odd number of elements,
+    as torch.cat hands them back, give what their copies give."""
+    rot = AxisRotary(4, 2, interleaved=interleaved)
+    g = torch.Generator(device=dev).manual_seed(3)
+
+    def n(*s):
+        return torch.randn(s, generator=g, device=dev).to(dtype)
+
+    pos = torch.rand((5, 2), generator=g, device=dev)
+    for flat in (False, True):
+        x, extra = n(5, 2, 4).requires_grad_(True), n(3) if flat else n(5, 3)
+        y = rot(x, pos)
+        joined = torch.cat([extra, y.flatten(0 if flat else 1)], -1)
+        w = n(*joined.shape)
+        dx, = torch.autograd.grad(joined, x, w)
+        part = w[3:].view(5, 2, 4) if flat else w[:, 3:].reshape(5, 2, 4)
+        want, = torch.autograd.grad(rot(x, pos), x, part.clone())
+        assert torch.equal(dx, want)
+        # the same layouts as inputs
+        view = w[3:].view(5, 2, 4) if flat else w[:, 3:].unflatten(1, (2, 4))
+        assert torch.equal(rot(view, pos), rot(view.clone(), pos))
+    binding.check_status()
