@@ -29,6 +29,13 @@ from torch.autograd.function import once_differentiable
 from . import binding
 
 
+def _packed(t):
+    """t contiguous and 16-byte aligned, as the attention and the feed-forward
+    block take it; a copy where it is not (part of a longer row, say)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class KmipAttentionFunction(torch.autograd.Function):
     """Autograd wrapper of kmip_attn_fwd / kmip_attn_bwd.
 
@@ -39,7 +46,7 @@ class KmipAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, Q, K, V, offsets, k: int, scale: float):
-        Q, K, V = Q.contiguous(), K.contiguous(), V.contiguous()
+        Q, K, V = _packed(Q), _packed(K), _packed(V)
         out, idx, lse = binding.attn_fwd(Q, K, V, k, scale, offsets)
         ctx.save_for_backward(Q, K, V, idx, lse)
         ctx.scale = scale
@@ -49,7 +56,7 @@ class KmipAttentionFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout, _didx):
         Q, K, V, idx, lse = ctx.saved_tensors
-        dQ, dK, dV = binding.attn_bwd(dout.contiguous().to(Q.dtype), Q, K, V, idx, lse,
+        dQ, dK, dV = binding.attn_bwd(_packed(dout.to(Q.dtype)), Q, K, V, idx, lse,
                                       ctx.scale)
         return dQ.to(Q.dtype), dK.to(K.dtype), dV.to(V.dtype), None, None, None
 
@@ -185,7 +192,7 @@ class GatedFeedForwardFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, wg, wu, wd, act: str):
-        x, wg, wu, wd = x.contiguous(), wg.contiguous(), wu.contiguous(), wd.contiguous()
+        x, wg, wu, wd = _packed(x), _packed(wg), _packed(wu), _packed(wd)
         ctx.save_for_backward(x, wg, wu, wd)
         ctx.act = act
         return binding.ffn_fwd(x, wg, wu, wd, act)
@@ -194,7 +201,7 @@ class GatedFeedForwardFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         x, wg, wu, wd = ctx.saved_tensors
-        return (*binding.ffn_bwd(dy.contiguous(), x, wg, wu, wd, ctx.act), None)
+        return (*binding.ffn_bwd(_packed(dy), x, wg, wu, wd, ctx.act), None)
 
 
 class GatedFeedForward(torch.nn.Module):

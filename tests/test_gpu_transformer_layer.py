@@ -229,3 +229,48 @@ def test_rotary_of_odd_strides_and_addresses(dev, dtype, interleaved):
         view = w[3:].view(5, 2, 4) if flat else w[:, 3:].unflatten(1, (2, 4))
         assert torch.equal(rot(view, pos), rot(view.clone(), pos))
     binding.check_status()
+
+
+def _behind(t, n):
+    """t's values as a contiguous view, n elements into its storage."""
+    buf = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)
+    buf[n:] = t.detach().flatten()
+    return buf[n:].view(t.shape)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_feed_forward_at_any_address(dev, dtype):
+    """Rows, weights and gradients that lie behind other elements."""
+    torch.manual_seed(2)
+    ffn = GatedFeedForward(32, 48, dtype=dtype, device=dev)
+    x, gy = (torch.randn(30, 32, device=dev).to(dtype) for _ in range(2))
+    leaves = [x.clone().requires_grad_(True), ffn.gate, ffn.up, ffn.down]
+    y = ffn(leaves[0])
+    want = torch.autograd.grad(y, leaves, gy)
+    moved = GatedFeedForward(32, 48, dtype=dtype, device=dev)
+    for name in ("gate", "up", "down"):
+        setattr(moved, name, torch.nn.Parameter(_behind(getattr(ffn, name), 3)))
+    leaves = [_behind(x, 1).requires_grad_(True), moved.gate, moved.up, moved.down]
+    y2 = moved(leaves[0])
+    got = torch.autograd.grad(torch.cat([torch.zeros_like(gy[0, :3]), y2.flatten()]), leaves,
+                              torch.cat([gy[0, :3], gy.flatten()]))
+    assert torch.equal(y, y2)
+    for a, c in zip(got, want):
+        assert torch.equal(a, c)
+
+
+def test_attention_at_any_address(dev):
+    from graph_transformer_sparse_kmip_b200.layer import kmip_attention
+    g = torch.Generator(device=dev).manual_seed(4)
+    q, k, v, gy = (torch.randn((40, 2, 32), generator=g, device=dev).to(BF) for _ in range(4))
+    leaves = [t.clone().requires_grad_(True) for t in (q, k, v)]
+    y, idx = kmip_attention(*leaves, 5)
+    want = torch.autograd.grad(y, leaves, gy)
+    leaves = [_behind(t, 1).requires_grad_(True) for t in (q, k, v)]
+    y2, idx2 = kmip_attention(*leaves, 5)
+    got = torch.autograd.grad(torch.cat([gy[0, 0, :3], y2.flatten()]), leaves,
+                              torch.cat([gy[0, 0, :3], gy.flatten()]))
+    assert torch.equal(y, y2) and torch.equal(idx, idx2)
+    assert torch.equal(got[0], want[0])
+    for a, c in zip(got[1:], want[1:]):     # fp32 atomic sums, rounded to bf16
+        assert (a.float() - c.float()).norm() <= 4e-3 * c.float().norm()
