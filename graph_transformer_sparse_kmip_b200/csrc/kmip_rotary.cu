@@ -322,6 +322,9 @@ extern "C" __attribute__((visibility("default"))) kmip_status_t kmip_rotary(
   if (2 * pairs > d) return KMIP_ERR_INVALID_ARG;
   if (N == 0) return KMIP_OK;
   if (!x || !out || !pos || (pairs && (!freq || !axis))) return KMIP_ERR_INVALID_ARG;
+  // the stride of a single row or head says nothing
+  if (N == 1) x_row = out_row = 0;
+  if (H == 1) x_head = out_head = 0;
   const bool in_place = x == out;
   if (in_place && (x_row != out_row || x_head != out_head)) return KMIP_ERR_INVALID_ARG;
   const size_t esize = dtype == KMIP_BF16 ? 2 : 4;

@@ -285,7 +285,8 @@ typedef enum {
  * the negative angle: that is the backward pass with respect to x.
  *   x          N rows of H heads of d elements; element (n, h, e) is at
  *              x[n * x_row + h * x_head + e] (strides in elements, so q and k
- *              can be turned where a fused projection wrote them).
+ *              can be turned where a fused projection wrote them; of a single
+ *              row or head the stride is not looked at).
  *   pos        [N, axes] of pos_type.
  *   freq       double [pairs], radians per unit; axis int32 [pairs], each in
  *              [0, axes).  An entry outside records KMIP_ERR_BAD_INDEX and its

@@ -209,3 +209,23 @@ def test_out_is_returned_and_checked(dev):
     with pytest.raises(TypeError, match="dtype"):
         binding.rotary(x.double(), pos, freq, axis)
     binding.check_status()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_strides_of_single_rows_and_heads_do_not_matter(dev, dtype, interleaved):
+    """A dimension of one has whatever stride the view it came from left."""
+    freq, axis = _table(16, 1, dev)
+    for N, H, strides in ((5, 1, (34, 33, 1)), (1, 5, (33, 32, 1)), (1, 1, (7, 5, 1)),
+                          (5, 1, (32, 0, 1)), (1, 1, (0, 0, 1))):
+        base, pos = torch.randn(400, device=dev).to(dtype), torch.rand((N, 1), device=dev)
+        x = base.as_strided((N, H, 32), strides)
+        want = binding.rotary(x.clone(memory_format=torch.contiguous_format), pos, freq, axis,
+                              interleaved=interleaved)
+        assert torch.equal(binding.rotary(x, pos, freq, axis, interleaved=interleaved), want)
+        out = torch.zeros(400, dtype=dtype, device=dev).as_strided((N, H, 32), strides)
+        assert torch.equal(binding.rotary(x, pos, freq, axis, interleaved=interleaved, out=out),
+                           want)
+        assert torch.equal(binding.rotary(x, pos, freq, axis, interleaved=interleaved, out=x),
+                           want)
+    binding.check_status()
