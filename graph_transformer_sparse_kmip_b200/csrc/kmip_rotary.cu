@@ -302,6 +302,29 @@ int unit_width(const RotaryParams& p) {
   return v;
 }
 
+// Whether N rows of H heads of d elements at x and at out, `delta` elements
+// further on, share one.  Blocks read and write in no order, so they may not.
+// With the same strides the two may lie between one another (other heads of
+// the same rows); with different ones they are taken to meet as soon as the
+// ranges that they span do.
+bool shares_elements(int64_t delta, int64_t N, int64_t H, int64_t d, int64_t x_row,
+                     int64_t x_head, int64_t out_row, int64_t out_head) {
+  const int64_t x_span = (N - 1) * x_row + (H - 1) * x_head + d;
+  const int64_t out_span = (N - 1) * out_row + (H - 1) * out_head + d;
+  if (delta >= x_span || delta <= -out_span) return false;
+  if (x_row != out_row || x_head != out_head) return true;
+  for (int64_t j = 1 - H; j < H; ++j) {
+    const int64_t rest = delta - j * x_head;  // to be met by a difference of rows
+    const int64_t i = x_row ? rest / x_row : 0;     // the closest is i, i - 1 or i + 1
+    for (int64_t r = i - 1; r <= i + 1; ++r) {
+      if (r <= -N || r >= N) continue;
+      const int64_t gap = rest - r * x_row;
+      if (gap < d && gap > -d) return true;
+    }
+  }
+  return false;
+}
+
 }  // namespace
 }  // namespace kmip
 
@@ -339,6 +362,11 @@ extern "C" __attribute__((visibility("default"))) kmip_status_t kmip_rotary(
       (N > 1 && H > 1 && out_row < d) ||
       (N > 1 && H > 1 && out_head < out_row && (H - 1) * out_head + d > out_row) ||
       (N > 1 && H > 1 && out_row <= out_head && (N - 1) * out_row + d > out_head))
+    return KMIP_ERR_INVALID_ARG;
+  const int64_t delta = static_cast<int64_t>(reinterpret_cast<uintptr_t>(out) -
+                                             reinterpret_cast<uintptr_t>(x)) /
+                        static_cast<int64_t>(esize);
+  if (!in_place && shares_elements(delta, N, H, d, x_row, x_head, out_row, out_head))
     return KMIP_ERR_INVALID_ARG;
   int* status = status_ptr();
   if (!status) return KMIP_ERR_CUDA;

@@ -292,7 +292,9 @@ typedef enum {
  *              [0, axes).  An entry outside records KMIP_ERR_BAD_INDEX and its
  *              pair is left unturned.
  *   out        as x with its own strides; out == x (with the same strides)
- *              turns in place, otherwise the two may not overlap.
+ *              turns in place, otherwise the two may not share an element,
+ *              nor, with different strides, the range they span
+ *              (KMIP_ERR_INVALID_ARG).
  * Angles are formed and reduced in fp64, so positions far from zero keep
  * their angle; the turn itself is fp32, rounded once.
  * Supported: d even, 2..512; H <= 4096; axes <= 64; 0 <= 2 pairs <= d.  x and

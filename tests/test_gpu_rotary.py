@@ -229,3 +229,22 @@ def test_strides_of_single_rows_and_heads_do_not_matter(dev, dtype, interleaved)
         assert torch.equal(binding.rotary(x, pos, freq, axis, interleaved=interleaved, out=x),
                            want)
     binding.check_status()
+
+
+def test_out_between_the_heads_of_x(dev):
+    """Other heads of the same rows are another tensor."""
+    g = torch.Generator(device=dev).manual_seed(1)
+    qkv = torch.randn((300, 12, 32), generator=g, device=dev).to(BF)
+    pos = torch.rand((300, 1), generator=g, device=dev)
+    freq, axis = _table(16, 1, dev)
+    q, k, keep = qkv[:, :4], qkv[:, 4:8], qkv.clone()
+    want = binding.rotary(q, pos, freq, axis)
+    binding.rotary(q, pos, freq, axis, out=k)
+    assert torch.equal(k, want) and torch.equal(qkv[:, :4], keep[:, :4])
+    assert torch.equal(qkv[:, 8:], keep[:, 8:])
+    with pytest.raises(KmipError) as e:
+        binding.rotary(q, pos, freq, axis, out=qkv[:, 3:7])
+    assert e.value.code == 1
+    with pytest.raises(KmipError):
+        binding.rotary(qkv[:299], pos[:299], freq, axis, out=qkv[1:])
+    binding.check_status()

@@ -181,3 +181,57 @@ def test_module_refusals():
     for channels, groups in ((32, 0), (32, 5), (32, -4)):
         with pytest.raises(ValueError):
             GraphGroupNorm(channels, groups)
+
+
+def test_rotary_refuses_an_out_that_overlaps(lib):
+    # heads of 32 elements (64 bytes), two to a row of 64: x takes 512 bytes
+    for kw in (dict(out=A + 64), dict(out=A + 2), dict(out=A - 2), dict(out=A + 128),
+               dict(out=A - 128), dict(out=A + 448), dict(out=A - 448), dict(out=A + 510),
+               # rows of 128 elements, the other half of each free
+               dict(x_row=128, out_row=128, out=A + 64), dict(x_row=128, out_row=128, out=A + 126),
+               dict(x_row=128, out_row=128, out=A + 256), dict(x_row=128, out_row=128, out=A - 66),
+               dict(x_row=128, out_row=128, out=A + 256 + 130),
+               # heads outermost
+               dict(x_row=32, x_head=128, out_row=32, out_head=128, out=A + 192),
+               dict(x_row=32, x_head=128, out_row=32, out_head=128, out=A - 256),
+               # other strides: by the ranges
+               dict(x_row=128, out=A + 128), dict(out_row=128, out=A - 256),
+               dict(x_head=0, x_row=32, out=A + 64),
+               # one row, one head
+               dict(N=1, out=A + 64), dict(N=1, out=A + 32), dict(H=1, N=1, out=A + 62),
+               dict(H=1, x_row=64, out_row=64, out=A + 62)):
+        assert _rotary(lib, **kw) == INVALID, kw
+
+
+def test_rotary_overlap_rule_against_sets_of_elements(tmp_path):
+    """The rule itself, compiled on the host, for all small layouts."""
+    import os
+    import re
+    import subprocess
+    from graph_transformer_sparse_kmip_b200.build import CSRC, CXX
+    text = open(os.path.join(CSRC, "kmip_rotary.cu")).read()
+    rule = re.search(r"bool shares_elements\(.*?\n}\n", text, re.S).group(0)
+    src, so = tmp_path / "rule.cpp", tmp_path / "rule.so"
+    src.write_text("#include <cstdint>\n" + rule + """
+extern "C" bool rule(int64_t delta, int64_t N, int64_t H, int64_t d, int64_t a, int64_t b,
+                     int64_t c, int64_t e) { return shares_elements(delta, N, H, d, a, b, c, e); }
+""")
+    subprocess.run([CXX, "-shared", "-fPIC", "-o", str(so), str(src)], check=True)
+    fn = ctypes.CDLL(str(so)).rule
+    fn.argtypes, fn.restype = [ctypes.c_int64] * 8, ctypes.c_bool
+    seen = [0, 0]
+    for N, H, d in ((1, 1, 2), (3, 1, 2), (1, 3, 2), (3, 2, 2), (2, 3, 4)):
+        for row, head in ((H * d, d), (2 * H * d, d), (2 * H * d + 1, d + 1), (d, N * d),
+                          (2 * d, 2 * N * d + 3)):
+            if N == 1:
+                row = 0
+            if H == 1:
+                head = 0
+            x = {n * row + h * head + e for n in range(N) for h in range(H) for e in range(d)}
+            for delta in range(-60, 61):
+                if delta == 0:
+                    continue
+                meet = any(v + delta in x for v in x)
+                assert fn(delta, N, H, d, row, head, row, head) == meet, (N, H, d, row, head, delta)
+                seen[meet] += 1
+    assert min(seen) > 100
