@@ -200,6 +200,8 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      pairs, interleaved, inverse, N, h, width, out(y), y.stride(0), y.stride(1),
                      stream_of(x), dtype),
             "kmip_rotary");
+      // autograd learns that what it may have saved has changed
+      if (given && !given->is_inference()) given->unsafeGetTensorImpl()->bump_version();
     }
     return THPVariable_Wrap(y);
   });

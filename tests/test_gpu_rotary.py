@@ -248,3 +248,25 @@ def test_out_between_the_heads_of_x(dev):
     with pytest.raises(KmipError):
         binding.rotary(qkv[:299], pos[:299], freq, axis, out=qkv[1:])
     binding.check_status()
+
+
+def test_a_turn_in_place_is_seen_by_autograd(dev):
+    """A tensor that the backward pass needs and that was turned since raises."""
+    pos = torch.rand((5, 1), device=dev)
+    freq, axis = _table(16, 1, dev)
+    for stream in (None, torch.cuda.current_stream()):
+        x = torch.randn((5, 2, 32), device=dev, requires_grad=True)
+        y = x * 2
+        loss = y.square().sum()
+        version = y._version
+        binding.rotary(y, pos, freq, axis, out=y, stream=stream)
+        assert y._version == version + 1
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():
+        z = torch.randn((5, 2, 32), device=dev)
+        binding.rotary(z, pos, freq, axis, out=z)
+    binding.rotary(z, pos, freq, axis, out=z)
+    fresh = torch.randn((5, 2, 32), device=dev)
+    assert binding.rotary(fresh, pos, freq, axis)._version == 0 and fresh._version == 0
+    binding.check_status()
