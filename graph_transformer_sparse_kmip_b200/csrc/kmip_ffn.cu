@@ -27,23 +27,6 @@ bool all_aligned(P... ptrs) {
   return (... && (ptrs && aligned16(ptrs)));
 }
 
-struct Span {
-  const void* p;
-  size_t bytes;
-};
-
-// Whether two of the spans share bytes, one of them among the first `outs`.
-template <size_t N>
-bool overlapping(const Span (&s)[N], size_t outs) {
-  for (size_t i = 0; i < outs; ++i)
-    for (size_t j = i + 1; j < N; ++j) {
-      const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p);
-      const uintptr_t b = reinterpret_cast<uintptr_t>(s[j].p);
-      if (a < b + s[j].bytes && b < a + s[i].bytes) return true;
-    }
-  return false;
-}
-
 size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 }  // namespace

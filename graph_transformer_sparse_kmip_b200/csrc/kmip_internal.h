@@ -100,6 +100,24 @@ cudaError_t launch_bwd_deterministic(kmip_dtype_t dtype, const BwdArgs& a, cudaS
 // next steps, past the last row, stay within an int.
 constexpr int64_t kMaxRows = INT32_MAX - (1 << 20);
 
+// Bytes of an argument (none where it is absent).
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+// Whether two of the spans share bytes, one of them among the first `outs`.
+template <size_t N>
+inline bool overlapping(const Span (&s)[N], size_t outs) {
+  for (size_t i = 0; i < outs; ++i)
+    for (size_t j = i + 1; j < N; ++j) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p);
+      const uintptr_t b = reinterpret_cast<uintptr_t>(s[j].p);
+      if (s[i].bytes && s[j].bytes && a < b + s[j].bytes && b < a + s[i].bytes) return true;
+    }
+  return false;
+}
+
 int device_sm_count();
 
 // Stream-ordered allocation from the library's own memory pool on the

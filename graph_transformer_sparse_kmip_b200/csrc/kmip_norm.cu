@@ -462,6 +462,13 @@ extern "C" __attribute__((visibility("default"))) kmip_status_t kmip_group_norm_
   if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(weight, es) ||
       !aligned_to(bias, es))
     return KMIP_ERR_INVALID_ARG;
+  const int G = graph_offsets ? num_graphs : 1;
+  const size_t nc = es * N * C, c = weight ? es * C : 0, stats = sizeof(float) * G * groups;
+  const size_t off = graph_offsets ? sizeof(int32_t) * ((size_t)G + 1) : 0;
+  if (overlapping({{y, nc}, {mean, stats}, {rstd, stats}, {x, y == x ? 0 : nc}, {weight, c},
+                   {bias, c}, {graph_offsets, off}}, 3) ||
+      overlapping({{x, nc}, {mean, stats}, {rstd, stats}}, 1))
+    return KMIP_ERR_INVALID_ARG;
   NormParams p{};
   p.x = x;
   p.w = weight;
@@ -472,7 +479,7 @@ extern "C" __attribute__((visibility("default"))) kmip_status_t kmip_group_norm_
   p.offsets = graph_offsets;
   p.N = (int)N;
   p.C = C;
-  p.G = graph_offsets ? num_graphs : 1;
+  p.G = G;
   p.groups = groups;
   p.cg = C / groups;
   p.eps = eps;
@@ -492,11 +499,17 @@ extern "C" __attribute__((visibility("default"))) kmip_status_t kmip_group_norm_
   if (!mean || !rstd || (N > 0 && (!x || !dy || !dx)) || !weight != !bias)
     return KMIP_ERR_INVALID_ARG;
   if (weight && (!dweight || !dbias)) return KMIP_ERR_INVALID_ARG;
-  if (N > 0 && dx == x) return KMIP_ERR_INVALID_ARG;
   const size_t es = dtype == KMIP_BF16 ? 2 : 4;
   if (!aligned_to(x, es) || !aligned_to(dy, es) || !aligned_to(dx, es) ||
       !aligned_to(weight, es) || !aligned_to(bias, es) || !aligned_to(dweight, es) ||
       !aligned_to(dbias, es))
+    return KMIP_ERR_INVALID_ARG;
+  const int G = graph_offsets ? num_graphs : 1;
+  const size_t nc = es * N * C, c = weight ? es * C : 0, stats = sizeof(float) * G * groups;
+  const size_t off = graph_offsets ? sizeof(int32_t) * ((size_t)G + 1) : 0;
+  if (overlapping({{dx, nc}, {dweight, c}, {dbias, c}, {dy, dx == dy ? 0 : nc}, {x, nc},
+                   {weight, c}, {bias, c}, {mean, stats}, {rstd, stats}, {graph_offsets, off}}, 3) ||
+      overlapping({{dy, nc}, {dweight, c}, {dbias, c}}, 1))
     return KMIP_ERR_INVALID_ARG;
   NormParams p{};
   p.x = x;
@@ -509,7 +522,7 @@ extern "C" __attribute__((visibility("default"))) kmip_status_t kmip_group_norm_
   p.offsets = graph_offsets;
   p.N = (int)N;
   p.C = C;
-  p.G = graph_offsets ? num_graphs : 1;
+  p.G = G;
   p.groups = groups;
   p.cg = C / groups;
   p.status = status_ptr();

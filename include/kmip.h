@@ -313,7 +313,8 @@ kmip_status_t kmip_rotary(const void* x, int64_t x_row, int64_t x_head, const vo
  *   mean, var  over the nodes of g and the channels of j (biased variance)
  *   rstd     = 1 / sqrt(var + eps)
  *   y        = act((x - mean) * rstd * weight + bias)
- *   x, y       [N, C] of `dtype` row-major; y may be x.
+ *   x, y       [N, C] of `dtype` row-major; y may be x.  Otherwise outputs may
+ *              not overlap inputs or one another (KMIP_ERR_INVALID_ARG).
  *   weight, bias  [C] of `dtype`, or both NULL (1 and 0).
  *   graph_offsets as in kmip_attn_fwd (NULL: one graph).  Each graph's range
  *              is checked on the device: a malformed one records
@@ -340,8 +341,9 @@ kmip_status_t kmip_group_norm_fwd(const void* x, const void* weight, const void*
  *   dx      = rstd (dz weight - m1 - xhat m2)  (of `dtype`, [N, C])
  * m1, m2 = means of dz weight and dz weight xhat over the graph and group.
  * dweight and dbias are written when weight is given (then they may not be
- * NULL).  dx may be dy, and may not be x.  Sums are joined in a fixed order:
- * results do not change from run to run.
+ * NULL).  dx may be dy; otherwise outputs may not overlap inputs or one
+ * another (KMIP_ERR_INVALID_ARG).  Sums are joined in a fixed order: results
+ * do not change from run to run.
  */
 kmip_status_t kmip_group_norm_bwd(const void* dy, const void* x, const void* weight,
                                   const void* bias, const int32_t* graph_offsets,

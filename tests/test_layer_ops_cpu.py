@@ -235,3 +235,21 @@ extern "C" bool rule(int64_t delta, int64_t N, int64_t H, int64_t d, int64_t a, 
                 assert fn(delta, N, H, d, row, head, row, head) == meet, (N, H, d, row, head, delta)
                 seen[meet] += 1
     assert min(seen) > 100
+
+
+def test_group_norm_refuses_outputs_that_overlap(lib):
+    # x, y, dy and dx take 512 bytes here, parameters 64, statistics 16
+    B = 8 * A
+    fwd = dict(x=A, w=2 * A, b=3 * A, y=4 * A, mean=5 * A, rstd=6 * A)
+    for kw in (dict(y=A + 2), dict(y=A - 510), dict(y=2 * A + 62), dict(b=B, y=B),
+               dict(mean=6 * A), dict(mean=6 * A + 12), dict(rstd=4 * A + 508), dict(mean=A + 508),
+               dict(rstd=2 * A), dict(y=A, mean=A + 16), dict(off=B, y=B + 4),
+               dict(off=B, mean=B + 4), dict(rstd=A - 12)):
+        assert _norm_fwd(lib, **{**fwd, **kw}) == INVALID, kw
+    bwd = dict(dy=A, x=2 * A, w=3 * A, b=4 * A, mean=5 * A, rstd=6 * A, dx=7 * A, dw=9 * A,
+               db=10 * A)
+    for kw in (dict(dx=2 * A), dict(dx=2 * A + 16), dict(dx=A + 16), dict(dx=A - 510),
+               dict(dw=10 * A), dict(db=9 * A + 62), dict(dw=3 * A), dict(db=4 * A + 2),
+               dict(dw=7 * A + 510), dict(db=2 * A), dict(dw=A), dict(dx=A, dw=A + 32),
+               dict(dx=5 * A + 12), dict(db=6 * A), dict(off=B, dw=B + 4), dict(off=B, dx=B - 508)):
+        assert _norm_bwd(lib, **{**bwd, **kw}) == INVALID, kw
