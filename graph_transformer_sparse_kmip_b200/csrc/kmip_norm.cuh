@@ -341,22 +341,19 @@ __device__ __forceinline__ void load_affine(const NormParams& p, int c,
   }
 }
 
-// z = x a + c for bf16, whose inputs carry 2^-9 of x already (the product's
-// rounding is 2^-24 of x rstd w); (x - mean) a + c for fp32, which takes the
-// difference first.
+// z = (x - mean) a + b with a = rstd w.  The difference comes first, for bf16
+// too: x a + (b - mean a) would be off by 2^-24 of mean rstd w, and rstd can be
+// 300 where all values of a group are alike.
 template <typename T, int V>
 struct Forward {
   static constexpr int P = Row<T, V>::P;
-  float2 a[P], c[P];
+  float2 a[P], b[P];
   float mean;
   __device__ void set(const NormParams& p, int ch, float m, float rs) {
-    load_affine<T, V>(p, ch, a, c);
+    load_affine<T, V>(p, ch, a, b);
     mean = m;
 #pragma unroll
-    for (int e = 0; e < P; ++e) {
-      a[e] = vmul<V>(a[e], splat2(rs));
-      if (sizeof(T) == 2) c[e] = vfma<V>(a[e], splat2(-m), c[e]);
-    }
+    for (int e = 0; e < P; ++e) a[e] = vmul<V>(a[e], splat2(rs));
   }
   template <int ACT>
   __device__ void apply(Row<T, V>& row) const {
@@ -364,8 +361,7 @@ struct Forward {
     row.get(f);
 #pragma unroll
     for (int e = 0; e < P; ++e) {
-      if (sizeof(T) == 4) f[e] = vadd<V>(f[e], splat2(-mean));
-      const float2 z = vfma<V>(f[e], a[e], c[e]);
+      const float2 z = vfma<V>(vadd<V>(f[e], splat2(-mean)), a[e], b[e]);
       f[e] = V > 1 ? act_value2<T, ACT>(z) : make_float2(act_value<T, ACT>(z.x), 0.f);
     }
     row.set(f);
@@ -390,8 +386,7 @@ struct Backward {
     grad.get(dz);
 #pragma unroll
     for (int e = 0; e < P; ++e) {
-      xh[e] = sizeof(T) == 2 ? vfma<V>(xh[e], splat2(rs), splat2(-mean * rs))
-                             : vmul<V>(vadd<V>(xh[e], splat2(-mean)), splat2(rs));
+      xh[e] = vmul<V>(vadd<V>(xh[e], splat2(-mean)), splat2(rs));
       const float2 z = vfma<V>(xh[e], w[e], b[e]);
       float2 f, g;
       if (V > 1) {

@@ -373,3 +373,42 @@ def test_many_graphs(dev, dtype, N, C, groups, G):
     sizes = [b - a for a, b in zip([0] + cut, cut + [N])]
     x, w, b, dy, off = _case(sizes, C, dtype, dev, seed=G)
     _check(x, w, b, dy, off, groups, "silu")
+
+
+ALIKE = pytest.mark.parametrize("sizes,C,groups", [
+    ([1, 700, 3], 64, 8), ([1] * 40, 64, 64), ([90000, 7], 128, 8), ([5, 70000], 129, 3),
+    ([600], 36, 6), ([3, 2], 4608, 1)])
+
+
+def _alike(sizes, C, value, dtype, dev):
+    x = torch.full((sum(sizes), C), value, device=dev).to(dtype)
+    w, b = torch.full_like(x[0], 2.0), torch.full_like(x[0], 0.5)
+    return x, w, b, wl.offsets_from_sizes(sizes).to(dev)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [1234.567, -1.0e6])
+@ALIKE
+def test_values_that_are_all_alike(dev, dtype, sizes, C, groups, value):
+    """Nodes whose features are one constant (padding, a single node with one
+    channel a group): x - mean is zero, so y is act(bias), whatever rstd."""
+    x, w, b, off = _alike(sizes, C, value, dtype, dev)
+    G = len(sizes)
+    y, mean, _ = binding.group_norm_fwd(x, w, b, groups, 1e-5, "none", off)
+    assert (mean == x[0, 0].float()).all()
+    assert (y.float() == 0.5).all()
+    # with the statistics that the definition has
+    rstd = torch.full((G, groups), 1e-5 ** -0.5, device=dev)
+    dy = torch.randn(x.shape, generator=torch.Generator(device=dev).manual_seed(1),
+                     device=dev).to(dtype)
+    dx, dw, db = binding.group_norm_bwd(dy, x, w, b, mean, rstd, groups, "none", off)
+    assert (dw == 0).all()
+    binding.check_status()
+
+
+def test_mean_far_from_zero_bf16(dev):
+    """As for fp32 below the half step of bf16: values around 1,000, a step of 4
+    apart, a dozen steps in all."""
+    x, w, b, dy, off = _case([900, 40], 64, BF, dev, seed=6, shift=0.0)
+    x = (x.float() * 8 + 1000.0).to(BF)
+    _check(x, w, b, dy, off, 4, "none")
