@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(NT, split_blocks(NT)) norm_stats_split(const N
   for (int slot = blockIdx.x; slot < p.slots; slot += gridDim.x) {
     int g, r0, r1;
     if (!slot_rows(p, slot, g, r0, r1)) continue;
-    slab_stats<T, V, NT, kRowsOne<V>>(p, s, r0, r1, sm);
+    slab_stats<T, V, NT, kRowsOne<V>>(p, s, p.offsets ? p.offsets[g] : 0, r0, r1, sm);
     if (threadIdx.x < s.ngroups)
       p.part[(int64_t)slot * p.groups + s.g0 + threadIdx.x] =
           make_double2(sm.gs0[threadIdx.x], sm.gq[threadIdx.x]);
@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(NT, split_blocks(NT)) norm_stats_split(const N
 }
 
 // One block per (graph, group): joins the graph's slots in a fixed order.
+template <typename T>
 __global__ void __launch_bounds__(256) norm_join_stats(const NormParams p) {
   after_previous();
   __shared__ double s0[8], s1[8];
@@ -61,7 +62,8 @@ __global__ void __launch_bounds__(256) norm_join_stats(const NormParams p) {
         q += s1[k];
       }
       float m, r;
-      finish_stats(x, q, (double)(hi - lo) * p.cg, p.eps, m, r);
+      const float c = lo < hi ? pivot_of<T>(p, lo, j) : 0.f;
+      finish_stats(x, q, (double)(hi - lo) * p.cg, c, p.eps, m, r);
       p.mean[i] = m;
       p.rstd[i] = r;
     }
@@ -70,6 +72,7 @@ __global__ void __launch_bounds__(256) norm_join_stats(const NormParams p) {
 }
 
 // The same for graphs of a few slots: one thread per (graph, group).
+template <typename T>
 __global__ void __launch_bounds__(256) norm_join_stats_few(const NormParams p) {
   after_previous();
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < (int64_t)p.G * p.groups;
@@ -85,7 +88,8 @@ __global__ void __launch_bounds__(256) norm_join_stats_few(const NormParams p) {
       x += v.x;
       q += v.y;
     }
-    finish_stats(x, q, (double)(hi - lo) * p.cg, p.eps, p.mean[i], p.rstd[i]);
+    const float c = lo < hi ? pivot_of<T>(p, lo, j) : 0.f;
+    finish_stats(x, q, (double)(hi - lo) * p.cg, c, p.eps, p.mean[i], p.rstd[i]);
   }
 }
 
@@ -349,11 +353,11 @@ cudaError_t norm_fwd(kmip_dtype_t dtype, int v, int act, NormParams p, cudaStrea
       norm_stats_split<T, V, NT><<<grid, NT, 0, stream>>>(p);
       const int64_t joins = (int64_t)p.G * p.groups;
       if (few_slots(p))
-        launch_next(norm_join_stats_few,
+        launch_next(norm_join_stats_few<T>,
                     dim3(joins < 65536 * 256ll ? (unsigned)((joins + 255) / 256) : 65536u), 256, 0,
                     stream, p);
       else
-        launch_next(norm_join_stats, dim3(joins < 65536 ? (unsigned)joins : 65536u), 256, 0,
+        launch_next(norm_join_stats<T>, dim3(joins < 65536 ? (unsigned)joins : 65536u), 256, 0,
                     stream, p);
       launch_next(norm_apply_split<T, V, ACT, NT>, grid, NT, 0, stream, p);
       return cudaGetLastError();

@@ -25,11 +25,16 @@
 //             reverse order, so that what the first pass left in L2 is met
 //             first.  Any graph size spreads over all SMs.
 //
-// Statistics that are not held: a thread keeps (n, mean, M2) and adds kRows x V
-// values at a time by their deviations from its mean; no difference of large
-// sums is formed in fp32.  Threads, and blocks, join in fp64 sums of n mean and
-// M2 + n mean^2.  All sums run in a fixed order: no atomics, the same bits
-// every run.
+// Means and variances are formed from differences, so that an offset common to
+// all values costs no digits and values that are all alike have variance 0.
+// Rows that are held add up in fp32, then their differences to that mean, which
+// correct it, and the squares.  Otherwise a thread keeps (n, mean, M2) and adds
+// kRows x V values at a time by their deviations from its mean; threads, and
+// blocks, join in fp64 sums of n (mean - c) and M2 + n (mean - c)^2, where c is
+// the group's first value: (mean - c)^2 is then at most n times the variance,
+// and the difference of the two keeps it to n 2^-53.  The backward's channel
+// sums are fp32 throughout, joined over threads, slots and graphs.  All sums run
+// in a fixed order: no atomics, the same bits every run.
 #pragma once
 
 #include "kmip_act.cuh"
@@ -251,15 +256,25 @@ struct StatSmem {
   float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
 };
 
-// Adds sum(n mean) and sum(M2 + n mean^2) of rows [r0, r1) to sm.gs0, sm.gq.
+// The value that a group's sums are relative to: its first, of the graph's row
+// lo (zero if that is not finite: the others' sums are to stay what they are).
+template <typename T>
+__device__ __forceinline__ float pivot_of(const NormParams& p, int lo, int group) {
+  const float v = (float)static_cast<const T*>(p.x)[(int64_t)lo * p.C + group * p.cg];
+  return fabsf(v) <= 3.4028234663852886e38f ? v : 0.f;
+}
+
+// Sets sm.gs0, sm.gq to sum(n (mean - c)) and sum(M2 + n (mean - c)^2) of rows
+// [r0, r1), c the pivots of the graph that begins at row lo.
 template <typename T, int V, int NT, int KR>
-__device__ void slab_stats(const NormParams& p, const Slab& s, int r0, int r1,
+__device__ void slab_stats(const NormParams& p, const Slab& s, int lo, int r0, int r1,
                            StatSmem<NT>& sm) {
   if (threadIdx.x < s.ngroups) sm.gs0[threadIdx.x] = sm.gq[threadIdx.x] = 0.0;
   for (int vt = 0; vt < s.vecs; vt += s.W) {
     const int v = vt + s.tx;
-    float n = 0.f, mean = 0.f, m2 = 0.f;
+    float n = 0.f, mean = 0.f, m2 = 0.f, pivot = 0.f;
     if (s.ty < s.TY && v < s.vecs) {
+      if (r0 < r1) pivot = pivot_of<T>(p, lo, s.g0 + v * V / p.cg);
       const T* const cols[1] = {static_cast<const T*>(p.x) + s.c0 + v * V};
       walk_rows<KR, T, V, 1>(s, r0, r1, p.C, cols, false, [&](Row<T, V> (&rows)[1][KR], int r) {
         // squared deviations from the running mean (at first from one of the
@@ -284,8 +299,9 @@ __device__ void slab_stats(const NormParams& p, const Slab& s, int r0, int r1,
         n = all;
       });
     }
-    sm.s0[threadIdx.x] = (double)n * mean;
-    sm.q[threadIdx.x] = (double)m2 + (double)n * mean * mean;
+    const double off = (double)mean - pivot;
+    sm.s0[threadIdx.x] = n * off;
+    sm.q[threadIdx.x] = m2 + n * off * off;
     __syncthreads();
     // one warp per group of this tile
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -313,12 +329,12 @@ __device__ void slab_stats(const NormParams& p, const Slab& s, int r0, int r1,
   }
 }
 
-__device__ __forceinline__ void finish_stats(double s0, double q, double count, float eps,
-                                             float& mean, float& rstd) {
+__device__ __forceinline__ void finish_stats(double s0, double q, double count, float pivot,
+                                             float eps, float& mean, float& rstd) {
   const double m = count > 0 ? s0 / count : 0.0;
   double var = count > 0 ? q / count - m * m : 0.0;
   var = var < 0.0 ? 0.0 : var;  // a NaN stays
-  mean = (float)m;
+  mean = (float)(pivot + m);
   rstd = (float)rsqrt(var + (double)eps);
 }
 

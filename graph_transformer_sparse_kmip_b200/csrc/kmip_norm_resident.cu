@@ -11,44 +11,55 @@
 namespace kmip {
 namespace {
 
-// Sum over all threads of this thread's group (one vector tile).  `vals` and
-// `sums` are shared, [NT] and [kMaxSlabGroups]; two calls in a row take
-// different ones.  Lanes of a warp add up first where the tile's layout is a
-// power of two (or one group is all there is); other layouts go through
-// shared memory thread by thread.
-template <int V, int NT>
-__device__ __forceinline__ float group_sum(const NormParams& p, const Slab& s, float mine,
-                                           float* vals, float* sums) {
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 plus(float2 a, float2 b) {
+  return make_float2(a.x + b.x, a.y + b.y);
+}
+__device__ __forceinline__ float from_lane(float a, int o) {
+  return __shfl_xor_sync(0xffffffffu, a, o);
+}
+__device__ __forceinline__ float2 from_lane(float2 a, int o) {
+  return make_float2(from_lane(a.x, o), from_lane(a.y, o));
+}
+
+// Sum over all threads of this thread's group (one vector tile) of a number or
+// a pair.  `vals` and `sums` are shared, [NT] and [kMaxSlabGroups]; two calls in
+// a row take different ones.  Lanes of a warp add up first where the tile's
+// layout is a power of two (or one group is all there is); other layouts go
+// through shared memory thread by thread.
+template <int V, int NT, typename S>
+__device__ __forceinline__ S group_sum(const NormParams& p, const Slab& s, S mine, S* vals,
+                                       S* sums) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = p.cg / V;
   if (s.ngroups == 1) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    for (int o = 16; o; o >>= 1) mine = plus(mine, from_lane(mine, o));
     if (lane == 0) vals[warp] = mine;
     __syncthreads();
-    float a = 0.f;
+    S a{};
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) a += vals[i];
+    for (int i = 0; i < NT / 32; ++i) a = plus(a, vals[i]);
     return a;
   }
   if (s.W <= 32 && (s.W & (s.W - 1)) == 0 && (w & (w - 1)) == 0) {
-    for (int o = 16; o >= s.W; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    for (int o = w >> 1; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    for (int o = 16; o >= s.W; o >>= 1) mine = plus(mine, from_lane(mine, o));
+    for (int o = w >> 1; o; o >>= 1) mine = plus(mine, from_lane(mine, o));
     const int j = s.tx / w;
     if (lane < s.W && lane % w == 0) vals[warp * s.ngroups + j] = mine;
     __syncthreads();
-    float a = 0.f;
+    S a{};
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) a += vals[i * s.ngroups + j];
+    for (int i = 0; i < NT / 32; ++i) a = plus(a, vals[i * s.ngroups + j]);
     return a;
   }
   vals[threadIdx.x] = mine;
   __syncthreads();
   for (int j = warp; j < s.ngroups; j += NT / 32) {
-    float a = 0.f;
+    S a{};
     for (int y = lane; y < s.TY; y += 32)
-      for (int i = 0; i < w; ++i) a += vals[y * s.W + j * w + i];
+      for (int i = 0; i < w; ++i) a = plus(a, vals[y * s.W + j * w + i]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    for (int o = 16; o; o >>= 1) a = plus(a, from_lane(a, o));
     if (lane == 0) sums[j] = a;
   }
   __syncthreads();
@@ -116,14 +127,20 @@ norm_fwd_resident(const NormParams p) {
         if (u * s.TY < mine) add_deviations<T, V>(held.get(u, 0), 0.f, sum, dev);
       const float count = (float)rows * (float)p.cg;
       float* v0 = reinterpret_cast<float*>(sm.s0);
-      float* v1 = reinterpret_cast<float*>(sm.q);
-      const float m = group_sum<V, NT>(p, s, sum.x + sum.y, v0, sm.mean) / count;
+      float2* v1 = reinterpret_cast<float2*>(sm.q);
+      const float near = group_sum<V, NT>(p, s, sum.x + sum.y, v0, sm.mean) / count;
       dev = sum = splat2(0.f);
 #pragma unroll kUnroll
       for (int u = 0; u < HOLD; ++u)
-        if (u * s.TY < mine) add_deviations<T, V>(held.get(u, 0), m, sum, dev);
-      const float var = group_sum<V, NT>(p, s, dev.x + dev.y, v1, sm.rstd) / count;
-      const float rs = 1.f / sqrtf(var + p.eps);
+        if (u * s.TY < mine) add_deviations<T, V>(held.get(u, 0), near, sum, dev);
+      // What the first sum lost is in the second: the mean of the differences to
+      // it.  (Not where they overflow.)
+      const float2 d = group_sum<V, NT>(p, s, make_float2(sum.x + sum.y, dev.x + dev.y), v1,
+                                        reinterpret_cast<float2*>(sm.gs0));
+      float by = d.x / count, less = by * d.x;
+      if (!isfinite(less)) by = less = 0.f;
+      const float m = near + by, var = (d.y - less) / count;
+      const float rs = 1.f / sqrtf((var < 0.f ? 0.f : var) + p.eps);  // a NaN stays
       if (s.ty == 0 && s.tx * V % p.cg == 0) {
         p.mean[at + s.tx * V / p.cg] = m;
         p.rstd[at + s.tx * V / p.cg] = rs;
@@ -141,10 +158,11 @@ norm_fwd_resident(const NormParams p) {
       __syncthreads();
       continue;
     }
-    slab_stats<T, V, NT, 2>(p, s, lo, hi, sm);
+    slab_stats<T, V, NT, 2>(p, s, lo, lo, hi, sm);
     if (threadIdx.x < s.ngroups) {
       float m, r;
-      finish_stats(sm.gs0[threadIdx.x], sm.gq[threadIdx.x], (double)rows * p.cg, p.eps, m, r);
+      const float c = rows ? pivot_of<T>(p, lo, s.g0 + threadIdx.x) : 0.f;
+      finish_stats(sm.gs0[threadIdx.x], sm.gq[threadIdx.x], (double)rows * p.cg, c, p.eps, m, r);
       sm.mean[threadIdx.x] = m;
       sm.rstd[threadIdx.x] = r;
       p.mean[at + threadIdx.x] = m;

@@ -412,3 +412,20 @@ def test_mean_far_from_zero_bf16(dev):
     x, w, b, dy, off = _case([900, 40], 64, BF, dev, seed=6, shift=0.0)
     x = (x.float() * 8 + 1000.0).to(BF)
     _check(x, w, b, dy, off, 4, "none")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("seed", range(4))
+@ALIKE
+def test_statistics_of_values_that_are_all_alike(dev, dtype, sizes, C, groups, seed):
+    """Their mean is the value and their variance zero, at any size: nothing is
+    subtracted that is not a difference to one of the values."""
+    g = torch.Generator().manual_seed(seed)
+    for value in (torch.randn(12, generator=g) * 100.0 ** seed).tolist():
+        x, w, b, off = _alike(sizes, C, value, dtype, dev)
+        y, mean, rstd = binding.group_norm_fwd(x, w, b, groups, 1e-5, "none", off)
+        binding.check_status()
+        assert (mean == x[0, 0].float()).all()
+        # one square root and one rounding
+        assert ((rstd.double() * 1e-5 ** 0.5 - 1).abs() <= 2.0 ** -22).all()
+        assert (y.float() == 0.5).all()
