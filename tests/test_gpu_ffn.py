@@ -210,3 +210,19 @@ def test_few_rows_see_the_projections_of_their_own_call(dev, dtype, N):
         for a, c in zip(got, want):
             assert torch.equal(a, c)
     binding.check_status()
+
+
+@pytest.mark.parametrize("N", [1, 20])
+def test_gelu_of_every_value(dev, N):
+    """x = e_0, Wu's first column 1 and Wd the identity hand out gelu of Wg's
+    first column: roundings to bf16 (twice the same) and 2^-16 of the value."""
+    z = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16).view(BF)
+    z = z[(z.float() >= -12.0) & (z.float() <= -0.5)]
+    z = z[: z.numel() // 8 * 8].to(dev)
+    F = z.numel()
+    x, wg, wu = (torch.zeros((n, F), dtype=BF, device=dev) for n in (N, F, F))
+    x[:, 0], wg[:, 0], wu[:, 0] = 1.0, z, 1.0
+    y = binding.ffn_fwd(x, wg, wu, torch.eye(F, dtype=BF, device=dev), "gelu")
+    ref = z.double() * 0.5 * torch.special.erfc(-z.double() / 2 ** 0.5)
+    assert ((y.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -16) * ref.abs()).all()
+    binding.check_status()

@@ -429,3 +429,33 @@ def test_statistics_of_values_that_are_all_alike(dev, dtype, sizes, C, groups, s
         # one square root and one rounding
         assert ((rstd.double() * 1e-5 ** 0.5 - 1).abs() <= 2.0 ** -22).all()
         assert (y.float() == 0.5).all()
+
+
+def _bf16_values(lo, hi, dev):
+    v = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16).view(BF)
+    v = v[(v.float() >= lo) & (v.float() <= hi) & (v.float().abs() >= 2.0 ** -20)]
+    return v[: v.numel() // 8 * 8].to(dev)
+
+
+@pytest.mark.parametrize("cg", [8, 2, 1])
+def test_gelu_of_every_value(dev, cg):
+    """With weight 0 the activation's argument is the bias.  One rounding, 2^-8,
+    and 2^-16 of the value: the tail of the normal distribution is good to
+    2^-17 down to -13, its density likewise."""
+    z = _bf16_values(-12.0, 12.0, dev)
+    C, zero = z.numel(), torch.zeros_like(z)
+    x = torch.randn((3, C), generator=torch.Generator(device=dev).manual_seed(0),
+                    device=dev).to(BF)
+    y, mean, rstd = binding.group_norm_fwd(x, zero, z, C // cg, 1e-5, "gelu")
+    v = z.double()
+    cdf = 0.5 * torch.special.erfc(-v / 2 ** 0.5)
+    assert ((y.double() - v * cdf).abs() <= (2.0 ** -8 + 2.0 ** -16) * (v * cdf).abs()).all()
+    # dbias of one node with dy = 1 is the slope
+    one = torch.ones((1, C), dtype=BF, device=dev)
+    _, _, db = binding.group_norm_bwd(one, x[:1].contiguous(), zero, z, mean, rstd, C // cg,
+                                      "gelu")
+    part = v * torch.exp(-0.5 * v * v) / (2 * torch.pi) ** 0.5
+    slope = cdf + part
+    assert ((db.double() - slope).abs()
+            <= 2.0 ** -8 * slope.abs() + 2.0 ** -16 * (cdf + part.abs())).all()
+    binding.check_status()
