@@ -10,6 +10,7 @@ CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -362,15 +363,17 @@ def load_host():
     hand it the entry points of the loaded library."""
     global _host
     if _host is None:
-        lib = load()
-        try:
-            from . import _kmip_host
-        except ImportError as e:
-            raise ImportError(f"the host module cannot be loaded ({e}); build it with "
-                              "`python -m graph_transformer_sparse_kmip_b200.build`") from e
-        _kmip_host.setup(KmipError, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-                                      for name in _HOST_CALLS))
-        _host = _kmip_host
+        from .build import host_path
+        lib, path = load(), host_path()
+        if not os.path.exists(path):
+            raise ImportError(f"{path} not found (the host module for this torch and Python); "
+                              "build it with `python -m graph_transformer_sparse_kmip_b200.build`")
+        spec = importlib.util.spec_from_file_location(__package__ + "._kmip_host", path)
+        host = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(host)
+        host.setup(KmipError, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                                for name in _HOST_CALLS))
+        _host = host
     return _host
 
 

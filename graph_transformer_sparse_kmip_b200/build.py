@@ -6,8 +6,10 @@ Each ``csrc/*.cu`` compiles to an object under ``_build/`` (skipped when the
 object is newer than every source and header), then all objects link into
 ``graph_transformer_sparse_kmip_b200/libkmip.so`` with the CUDA runtime
 linked statically, so the library needs only the driver at run time.
-``csrc/kmip_host.cpp`` becomes ``_kmip_host.so``, the module through which
-binding.py calls the operators around the attention (g++, torch's headers).
+``csrc/kmip_host.cpp`` becomes ``_kmip_host-<tag>.so``, the module through which
+binding.py calls the operators around the attention (g++, torch's headers).  It
+holds inline code of torch and of CPython, so the tag names their versions
+(host_path), and a module built for others is neither kept nor loaded.
 
 ``--debug-bounds`` builds ``libkmip_debug.so`` instead (objects under
 ``_build/debug/``) with KMIP_DEBUG_BOUNDS defined: the kernels then check
@@ -20,6 +22,7 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import hashlib
 import os
 import subprocess
 import sys
@@ -31,7 +34,6 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkmip.so")
 LIB_DEBUG = os.path.join(PKG, "libkmip_debug.so")
-HOST = os.path.join(PKG, "_kmip_host.so")
 NVCC = os.environ.get("NVCC", "nvcc")
 CXX = os.environ.get("CXX", "g++")
 
@@ -65,16 +67,25 @@ def _compile(src: str, force: bool, verbose: bool, debug: bool = False) -> str:
     return obj
 
 
+def host_path() -> str:
+    """The host module for this interpreter and this torch."""
+    import torch
+    made_for = (torch.__version__, torch.version.cuda, torch.version.git_version,
+                torch.compiled_with_cxx11_abi(), sysconfig.get_config_var("SOABI"))
+    tag = hashlib.sha1(repr(made_for).encode()).hexdigest()[:12]
+    return os.path.join(PKG, f"_kmip_host-{tag}.so")
+
+
 def _build_host(force: bool) -> None:
-    src = os.path.join(CSRC, "kmip_host.cpp")
+    src, host = os.path.join(CSRC, "kmip_host.cpp"), host_path()
     newest = max(os.path.getmtime(p) for p in (src, os.path.join(ROOT, "include", "kmip.h")))
-    if not force and os.path.exists(HOST) and os.path.getmtime(HOST) >= newest:
+    if not force and os.path.exists(host) and os.path.getmtime(host) >= newest:
         return
     import torch
     from torch.utils import cpp_extension
     dirs = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"],
             *cpp_extension.include_paths(device_type="cuda")]
-    tmp = f"{HOST}.{os.getpid()}.tmp"
+    tmp = f"{host}.{os.getpid()}.tmp"
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *(f for d in dirs for f in ("-isystem" if "torch" in d else "-I", d)), src, "-o", tmp,
@@ -83,7 +94,10 @@ def _build_host(force: bool) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{CXX} failed for {src}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, HOST)
+    os.replace(tmp, host)
+    for old in glob.glob(os.path.join(PKG, "_kmip_host*.so")):
+        if old != host:
+            os.remove(old)
 
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False,

@@ -253,3 +253,23 @@ def test_group_norm_refuses_outputs_that_overlap(lib):
                dict(dw=7 * A + 510), dict(db=2 * A), dict(dw=A), dict(dx=A, dw=A + 32),
                dict(dx=5 * A + 12), dict(db=6 * A), dict(off=B, dw=B + 4), dict(off=B, dx=B - 508)):
         assert _norm_bwd(lib, **{**bwd, **kw}) == INVALID, kw
+
+
+def test_host_module_belongs_to_its_torch_and_python(lib, monkeypatch):
+    """One that was built for others is not loaded, and named as what to build."""
+    import os
+    import sysconfig
+    from graph_transformer_sparse_kmip_b200 import build
+    here = build.host_path()
+    assert os.path.exists(here) and binding.load_host() is binding.load_host()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "1.0")
+        other = build.host_path()
+        assert other != here
+        m.setattr(binding, "_host", None)
+        with pytest.raises(ImportError, match="build it"):
+            binding.load_host()
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: "cpython-999")
+        assert build.host_path() not in (here, other)
+    assert build.host_path() == here
