@@ -450,7 +450,8 @@ __device__ void slab_apply(const NormParams& p, const Slab& s, int r0, int r1, c
 }
 
 // ---------------------------------------------------------------- backward
-// (Dynamic shared memory: at most 42 KB with 256 threads, 162 KB with 1,024.)
+// (At most 42 KB with 256 threads, 162 KB with 1,024; the resident kernels keep
+// 64 KB of rows beside it.)
 template <int NT, int V>
 struct BwdSmem {
   float red[2][NT * V / 2 * 3];  // [channel of the tile][TY, or TY + 1 if even]
@@ -592,8 +593,8 @@ __device__ __forceinline__ void load_stats(const NormParams& p, const Slab& s, i
   }
 }
 
-// The resident kernels (kmip_norm_resident.cu); p.gps is set.  norm_bwd_blocks:
-// rows of p.chan that the backward writes.
+// The resident kernels (kmip_norm_resident.cu); p.gps is set.
+// norm_resident_blocks: rows of p.chan that the backward writes.
 int norm_resident_blocks(const NormParams& p, int slabs);
 cudaError_t launch_norm_fwd_resident(kmip_dtype_t dtype, int v, int act, const NormParams& p,
                                      int slabs, cudaStream_t stream);

@@ -277,6 +277,7 @@ cudaError_t launch_norm_fwd_resident(kmip_dtype_t dtype, int v, int act, const N
     const auto run = [&]<int NT, int HOLD, bool SHARED>() {
       auto kern = norm_fwd_resident<T, V, ACT, NT, HOLD, SHARED>;
       constexpr int smem = SHARED ? HOLD * NT * 16 : 0;
+      static_assert(smem + sizeof(StatSmem<NT>) <= 232448, "shared memory");
       const cudaError_t e =
           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
@@ -298,7 +299,9 @@ cudaError_t launch_norm_bwd_resident(kmip_dtype_t dtype, int v, int act, const N
   return norm_dispatch(dtype, v, act, [&]<typename T, int V, int ACT>() {
     const auto run = [&]<int NT, int HOLD>() {
       auto kern = norm_bwd_resident<T, V, ACT, NT, HOLD>;
+      // up to 106 KB with 256 threads and 226 KB with 1,024, and the statistics
       constexpr int smem = (kWide<T, V> ? HOLD * 2 * NT * 16 : 0) + (int)sizeof(BwdSmem<NT, V>);
+      static_assert(smem + 2 * kMaxSlabGroups * 4 <= 232448, "shared memory");
       const cudaError_t e =
           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
