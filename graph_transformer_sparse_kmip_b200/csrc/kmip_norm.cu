@@ -19,9 +19,9 @@ __global__ void __launch_bounds__(NT, split_blocks(NT)) norm_stats_split(const N
   __shared__ StatSmem<NT> sm;
   const Slab s = make_slab<NT, V>(p, blockIdx.y);
   for (int slot = blockIdx.x; slot < p.slots; slot += gridDim.x) {
-    int g, r0, r1;
-    if (!slot_rows(p, slot, g, r0, r1)) continue;
-    slab_stats<T, V, NT, kRowsOne<V>>(p, s, p.offsets ? p.offsets[g] : 0, r0, r1, sm);
+    int g, lo, r0, r1;
+    if (!slot_rows(p, slot, g, lo, r0, r1)) continue;
+    slab_stats<T, V, NT, kRowsOne<V>>(p, s, lo, r0, r1, sm);
     if (threadIdx.x < s.ngroups)
       p.part[(int64_t)slot * p.groups + s.g0 + threadIdx.x] =
           make_double2(sm.gs0[threadIdx.x], sm.gq[threadIdx.x]);
@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(256) norm_join_stats(const NormParams p) {
     int lo, hi;
     if (!graph_rows(p, g, lo, hi)) continue;
     const int a = first_slot(p, g), n = (int)(((int64_t)hi - lo + p.R - 1) / p.R);
+    const T c = lo < hi ? first_of<T>(p, lo, j) : T(0.f);
     double x = 0.0, q = 0.0;
 #pragma unroll 4
     for (int t = threadIdx.x; t < n; t += 256) {
@@ -62,8 +63,7 @@ __global__ void __launch_bounds__(256) norm_join_stats(const NormParams p) {
         q += s1[k];
       }
       float m, r;
-      const float c = lo < hi ? pivot_of<T>(p, lo, j) : 0.f;
-      finish_stats(x, q, (double)(hi - lo) * p.cg, c, p.eps, m, r);
+      finish_stats(x, q, (double)(hi - lo) * p.cg, pivot_of(c), p.eps, m, r);
       p.mean[i] = m;
       p.rstd[i] = r;
     }
@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(256) norm_join_stats_few(const NormParams p) {
     int lo, hi;
     if (!graph_rows(p, g, lo, hi, true)) continue;
     const int a = first_slot(p, g), n = (int)(((int64_t)hi - lo + p.R - 1) / p.R);
+    const T c = lo < hi ? first_of<T>(p, lo, j) : T(0.f);
     double x = 0.0, q = 0.0;
 #pragma unroll 4
     for (int t = 0; t < n; ++t) {
@@ -88,8 +89,7 @@ __global__ void __launch_bounds__(256) norm_join_stats_few(const NormParams p) {
       x += v.x;
       q += v.y;
     }
-    const float c = lo < hi ? pivot_of<T>(p, lo, j) : 0.f;
-    finish_stats(x, q, (double)(hi - lo) * p.cg, c, p.eps, p.mean[i], p.rstd[i]);
+    finish_stats(x, q, (double)(hi - lo) * p.cg, pivot_of(c), p.eps, p.mean[i], p.rstd[i]);
   }
 }
 
@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(NT, split_blocks(NT)) norm_apply_split(const N
   __shared__ float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
   const Slab s = make_slab<NT, V>(p, blockIdx.y);
   for (int slot = p.slots - 1 - (int)blockIdx.x; slot >= 0; slot -= gridDim.x) {
-    int g, r0, r1;
-    if (!slot_rows(p, slot, g, r0, r1)) continue;
+    int g, lo, r0, r1;
+    if (!slot_rows(p, slot, g, lo, r0, r1)) continue;
     load_stats(p, s, g, mean, rstd);
     __syncthreads();
     slab_apply<T, V, ACT, kRowsOne<V>>(p, s, r0, r1, mean, rstd);
@@ -117,8 +117,8 @@ norm_bwd_sums_split(const NormParams p) {
   __shared__ float mean[kMaxSlabGroups], rstd[kMaxSlabGroups];
   const Slab s = make_slab<NT, V>(p, blockIdx.y);
   for (int slot = blockIdx.x; slot < p.slots; slot += gridDim.x) {
-    int g, r0, r1;
-    if (!slot_rows(p, slot, g, r0, r1)) continue;
+    int g, lo, r0, r1;
+    if (!slot_rows(p, slot, g, lo, r0, r1)) continue;
     load_stats(p, s, g, mean, rstd);
     __syncthreads();
     slab_bwd_sums<T, V, ACT, NT, false, kRowsTwo<V>>(
@@ -208,13 +208,13 @@ norm_bwd_apply_split(const NormParams p) {
   const Slab s = make_slab<NT, V>(p, blockIdx.y);
   int have = -1;
   for (int slot = p.slots - 1 - (int)blockIdx.x; slot >= 0; slot -= gridDim.x) {
-    int g, r0, r1;
-    if (!slot_rows(p, slot, g, r0, r1)) continue;
+    int g, lo, r0, r1;
+    if (!slot_rows(p, slot, g, lo, r0, r1)) continue;
     if (g != have) {  // means of the graph's groups, from its channel sums
       have = g;
       __syncthreads();
       load_stats(p, s, g, mean, rstd);
-      int lo, hi;
+      int hi;
       graph_rows(p, g, lo, hi);
       const float* src = p.gchan + (int64_t)g * 2 * p.C;
       const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

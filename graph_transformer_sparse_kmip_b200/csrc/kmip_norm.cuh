@@ -152,11 +152,11 @@ __device__ __forceinline__ int first_slot(const NormParams& p, int g) {
   return (p.offsets ? p.offsets[g] : 0) / p.R + g;
 }
 
-// Graph and rows of a slot; false when the slot holds none.  (The same plain
+// Graph (and its first row) and rows of a slot; false when the slot holds none.  (The same plain
 // search in every thread: everything that follows from it stays in uniform
 // registers.  A search by 32 probes of a warp made the backward's passes over
 // single elements a third slower.)
-__device__ __forceinline__ bool slot_rows(const NormParams& p, int slot, int& g, int& r0,
+__device__ __forceinline__ bool slot_rows(const NormParams& p, int slot, int& g, int& lo, int& r0,
                                           int& r1) {
   int a = 0, b = p.G - 1;  // last graph whose first slot is <= slot
   while (a < b) {
@@ -164,7 +164,7 @@ __device__ __forceinline__ bool slot_rows(const NormParams& p, int slot, int& g,
     if (first_slot(p, m) <= slot) a = m; else b = m - 1;
   }
   g = a;
-  int lo, hi;
+  int hi;
   if (!graph_rows(p, g, lo, hi)) return false;
   const int64_t at = lo + (int64_t)(slot - first_slot(p, g)) * p.R;
   if (at < lo || at >= hi) return false;
@@ -258,10 +258,14 @@ struct StatSmem {
 
 // The value that a group's sums are relative to: its first, of the graph's row
 // lo (zero if that is not finite: the others' sums are to stay what they are).
+// Loaded ahead of the rows, looked at behind them.
 template <typename T>
-__device__ __forceinline__ float pivot_of(const NormParams& p, int lo, int group) {
-  const float v = (float)static_cast<const T*>(p.x)[(int64_t)lo * p.C + group * p.cg];
-  return fabsf(v) <= 3.4028234663852886e38f ? v : 0.f;
+__device__ __forceinline__ T first_of(const NormParams& p, int lo, int group) {
+  return static_cast<const T*>(p.x)[(int64_t)lo * p.C + group * p.cg];
+}
+template <typename T>
+__device__ __forceinline__ float pivot_of(T first) {
+  return isfinite((float)first) ? (float)first : 0.f;
 }
 
 // Sets sm.gs0, sm.gq to sum(n (mean - c)) and sum(M2 + n (mean - c)^2) of rows
@@ -272,9 +276,10 @@ __device__ void slab_stats(const NormParams& p, const Slab& s, int lo, int r0, i
   if (threadIdx.x < s.ngroups) sm.gs0[threadIdx.x] = sm.gq[threadIdx.x] = 0.0;
   for (int vt = 0; vt < s.vecs; vt += s.W) {
     const int v = vt + s.tx;
-    float n = 0.f, mean = 0.f, m2 = 0.f, pivot = 0.f;
+    float n = 0.f, mean = 0.f, m2 = 0.f;
+    T c = T(0.f);
     if (s.ty < s.TY && v < s.vecs) {
-      if (r0 < r1) pivot = pivot_of<T>(p, lo, s.g0 + v * V / p.cg);
+      if (r0 < r1) c = first_of<T>(p, lo, s.g0 + v * V / p.cg);
       const T* const cols[1] = {static_cast<const T*>(p.x) + s.c0 + v * V};
       walk_rows<KR, T, V, 1>(s, r0, r1, p.C, cols, false, [&](Row<T, V> (&rows)[1][KR], int r) {
         // squared deviations from the running mean (at first from one of the
@@ -299,7 +304,7 @@ __device__ void slab_stats(const NormParams& p, const Slab& s, int lo, int r0, i
         n = all;
       });
     }
-    const double off = (double)mean - pivot;
+    const double off = (double)mean - pivot_of(c);
     sm.s0[threadIdx.x] = n * off;
     sm.q[threadIdx.x] = m2 + n * off * off;
     __syncthreads();

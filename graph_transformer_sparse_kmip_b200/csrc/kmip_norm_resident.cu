@@ -36,9 +36,9 @@ __device__ __forceinline__ S group_sum(const NormParams& p, const Slab& s, S min
     for (int o = 16; o; o >>= 1) mine = plus(mine, from_lane(mine, o));
     if (lane == 0) vals[warp] = mine;
     __syncthreads();
-    S a{};
+    S a = vals[lane % (NT / 32)];
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) a = plus(a, vals[i]);
+    for (int o = NT / 64; o; o >>= 1) a = plus(a, from_lane(a, o));
     return a;
   }
   if (s.W <= 32 && (s.W & (s.W - 1)) == 0 && (w & (w - 1)) == 0) {
@@ -161,7 +161,7 @@ norm_fwd_resident(const NormParams p) {
     slab_stats<T, V, NT, 2>(p, s, lo, lo, hi, sm);
     if (threadIdx.x < s.ngroups) {
       float m, r;
-      const float c = rows ? pivot_of<T>(p, lo, s.g0 + threadIdx.x) : 0.f;
+      const float c = rows ? pivot_of(first_of<T>(p, lo, s.g0 + threadIdx.x)) : 0.f;
       finish_stats(sm.gs0[threadIdx.x], sm.gq[threadIdx.x], (double)rows * p.cg, c, p.eps, m, r);
       sm.mean[threadIdx.x] = m;
       sm.rstd[threadIdx.x] = r;
