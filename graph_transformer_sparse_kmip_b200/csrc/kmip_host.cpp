@@ -4,9 +4,9 @@
 //
 // A call on one node or a small graph is bound by what happens before its
 // launch.  With these steps in Python and ctypes a rotary call on one node took
-// 11.9 us, a norm of 1,024 x 32 14.2 and one feed-forward row 13.5; here 7.0, 8.2
-// (its kernel) and 9.0.  Nothing is computed here: libkmip's C ABI is the
-// only thing called, at the addresses that binding.py hands over.
+// 11.9 us, a norm of 1,024 x 32 14.2 and one feed-forward row 13.5; here 5.3, 8.2
+// and 8.4 (of which its two kernels take 7).  Nothing is computed here: libkmip's
+// C ABI is the only thing called, at the addresses that binding.py hands over.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 

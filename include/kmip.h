@@ -321,8 +321,10 @@ kmip_status_t kmip_rotary(const void* x, int64_t x_row, int64_t x_head, const vo
  *              KMIP_ERR_BAD_OFFSETS; y, mean and rstd are then unspecified.
  *   mean, rstd fp32 [num_graphs, groups], overwritten (an empty graph: 0 and
  *              1 / sqrt(eps)); the backward takes them.
- * Statistics are held in fp32 (per thread, by batches with their own mean)
- * and joined in fp64; results do not change from run to run.
+ * Statistics are formed from differences to a value or a mean of the group, in
+ * fp32 per thread and joined in fp64 where rows do not fit on the chip, so an
+ * offset that all values share costs no digits, and values that are all alike
+ * have variance 0.  Results do not change from run to run.
  * Supported: N <= 2^31 - 2^20 - 1; 1 <= groups <= C <= 65536, groups divides C;
  * eps > 0.  x, y and
  * the parameters need only their element's alignment; 16-byte aligned rows
