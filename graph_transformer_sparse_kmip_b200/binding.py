@@ -403,7 +403,8 @@ def rotary(x, pos, freq, axis, inverse: bool = False, interleaved: bool = False,
     even one, from an address that a pair is aligned to), elements of a head
     adjacent; pos: [N, A] fp32, int32 or int64; freq: fp64 [P]; axis: int32
     [P].  out: a new contiguous tensor, or a tensor like x (x itself: in
-    place; otherwise it may share no element with x).  inverse=True is the gradient with respect to x."""
+    place; otherwise it may share no element with x).  inverse=True is the
+    gradient with respect to x."""
     fn = (_host or load_host()).rotary
     if stream is not None or _NVTX:
         return _aside(fn, stream, x, pos, freq, axis, inverse, interleaved, out)

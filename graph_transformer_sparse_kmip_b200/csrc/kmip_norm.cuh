@@ -152,10 +152,10 @@ __device__ __forceinline__ int first_slot(const NormParams& p, int g) {
   return (p.offsets ? p.offsets[g] : 0) / p.R + g;
 }
 
-// Graph (and its first row) and rows of a slot; false when the slot holds none.  (The same plain
-// search in every thread: everything that follows from it stays in uniform
-// registers.  A search by 32 probes of a warp made the backward's passes over
-// single elements a third slower.)
+// Graph, its first row, and the rows of a slot; false when the slot holds none.
+// (The same plain search in every thread: everything that follows from it stays
+// in uniform registers.  A search by 32 probes of a warp made the backward's
+// passes over single elements a third slower.)
 __device__ __forceinline__ bool slot_rows(const NormParams& p, int slot, int& g, int& lo, int& r0,
                                           int& r1) {
   int a = 0, b = p.G - 1;  // last graph whose first slot is <= slot
